@@ -60,6 +60,15 @@ class moe_cluster_config(C.Structure):
                 ("cache_life", C.c_int32)]
 
 
+class moe_quant_config(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("n_in", "n_out", "group", "x_dtype")]
+
+
+class moe_quant_weights(C.Structure):
+    _fields_ = [("q", C.c_void_p), ("scale", C.c_void_p), ("values", C.c_void_p),
+                ("values_dtype", C.c_int32), ("on_device", C.c_int32)]
+
+
 class MoEError(RuntimeError):
     def __init__(self, code, msg):
         super().__init__(f"moe error {code}: {msg}")
@@ -101,6 +110,11 @@ def _load():
         "moe_cluster_regroup": ([P, P, P, P, P, P, P], C.c_int),
         "moe_compress_projection": ([C.c_int32, C.c_int32, P, C.c_int32, C.c_int32, C.c_int32, P, P, P, P, P,
                                      C.c_int32], C.c_int),
+        "moe_quant_create": ([C.POINTER(moe_quant_config), C.POINTER(moe_quant_weights), P, C.POINTER(P)], C.c_int),
+        "moe_quant_matvec": ([P, P, C.c_int64, C.c_int32, P, C.c_int64, P], C.c_int),
+        "moe_quant_read": ([P, P, P], C.c_int),
+        "moe_quant_bytes": ([P], C.c_int64),
+        "moe_quant_destroy": ([P], C.c_int),
         "moe_profile_begin": ([P, C.c_int32, C.c_int32], C.c_int),
         "moe_profile_end": ([P, P, C.c_int32, C.POINTER(C.c_int32), C.POINTER(C.c_int32),
                              C.c_char_p, C.c_int32], C.c_int),
@@ -351,6 +365,107 @@ class Layer:
     def close(self):
         if getattr(self, "h", None):
             lib.moe_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+# ------------------------------------------------- products with 4-bit weights --
+def _rows(t, n: int, dtype, name: str, device: int):
+    """Row count and row pitch of a 2-D tensor [T, n] with unit column stride."""
+    if t.dim() != 2 or t.shape[1] != n:
+        raise ValueError(f"{name}: expected [T, {n}], got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    if not t.is_cuda or t.device.index != device:
+        raise ValueError(f"{name}: expected a tensor on device {device}, got {t.device}")
+    if t.stride(1) != 1 and n > 1:
+        raise ValueError(f"{name}: the elements of a row must be consecutive")
+    if t.shape[0] > 1 and t.stride(0) < n:
+        raise ValueError(f"{name}: rows overlap (row pitch {t.stride(0)} < {n})")
+    return t.shape[0], (t.stride(0) if t.shape[0] > 1 else n)
+
+
+class QuantLinear:
+    """A matrix [n_in, n_out] in 4 bits with one fp16 scale per ``group`` input
+    rows, for products with a few rows (include/moe_quant.h).
+
+    Either codes ``q`` (int8 in [-8, 7]) with ``scale`` (float16 [ceil(n_in /
+    group), n_out]), or floating-point ``values`` to quantise.  All NumPy
+    arrays on the host, or all torch tensors on the current device.
+    """
+
+    def __init__(self, n_in: int, n_out: int, group: int, x_dtype: str, q=None, scale=None, values=None,
+                 stream=None):
+        import torch
+        cfg = moe_quant_config(n_in, n_out, group, DTYPE[x_dtype])
+        self.n_in, self.n_out, self.group = n_in, n_out, group
+        self.dtype = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}[x_dtype]
+        w, keep = moe_quant_weights(), []
+        given = [a for a in (q, scale, values) if a is not None]
+        w.on_device = 1 if given and all(isinstance(a, torch.Tensor) and a.is_cuda for a in given) else 0
+
+        def ptr(a, shape, kinds, name):
+            if a is None:
+                return None
+            if tuple(a.shape) != shape:
+                raise ValueError(f"{name}: expected shape {shape}, got {tuple(a.shape)}")
+            if isinstance(a, torch.Tensor):
+                if a.is_cuda and not w.on_device:
+                    raise ValueError("q, scale and values must all be on the device or all on the host")
+                a = a.contiguous()
+                kind = {torch.int8: "i8", torch.float16: "f16", torch.float32: "f32",
+                        torch.bfloat16: "bf16"}.get(a.dtype)
+                at = a.data_ptr()
+            else:
+                a = np.ascontiguousarray(a)
+                kind = {"int8": "i8", "float16": "f16", "float32": "f32", "uint16": "bf16"}.get(a.dtype.name)
+                at = a.ctypes.data
+            if kind not in kinds:
+                raise ValueError(f"{name}: unsupported dtype {a.dtype}")
+            keep.append(a)
+            if name == "values":
+                w.values_dtype = DTYPE[kind]
+            return at
+
+        w.q = ptr(q, (n_in, n_out), ("i8",), "q")
+        w.scale = ptr(scale, (-(-n_in // max(group, 1)), n_out), ("f16",), "scale")
+        w.values = ptr(values, (n_in, n_out), ("f32", "f16", "bf16"), "values")
+        h = C.c_void_p()
+        st = _stream_ptr(stream) if w.on_device else None
+        check(lib.moe_quant_create(C.byref(cfg), C.byref(w), st, C.byref(h)))
+        self.h = h
+        self.device = torch.cuda.current_device()
+
+    def matvec(self, X, Y=None, stream=None):
+        """Y = X W for X [T, n_in]; rows may be strided."""
+        import torch
+        T, ldx = _rows(X, self.n_in, self.dtype, "X", self.device)
+        if Y is None:
+            Y = torch.empty((T, self.n_out), dtype=self.dtype, device=X.device)
+        Ty, ldy = _rows(Y, self.n_out, self.dtype, "Y", self.device)
+        if Ty != T:
+            raise ValueError(f"Y has {Ty} rows, X has {T}")
+        check(lib.moe_quant_matvec(self.h, X.data_ptr(), ldx, T, Y.data_ptr(), ldy, _stream_ptr(stream)))
+        return Y
+
+    def read(self):
+        """(q int8 [n_in, n_out], scale float16 [ceil(n_in / group), n_out]) as stored."""
+        q = np.zeros((self.n_in, self.n_out), dtype=np.int8)
+        sc = np.zeros((-(-self.n_in // self.group), self.n_out), dtype=np.float16)
+        check(lib.moe_quant_read(self.h, q.ctypes.data, sc.ctypes.data))
+        return q, sc
+
+    def stored_bytes(self) -> int:
+        return lib.moe_quant_bytes(self.h)
+
+    def close(self):
+        if getattr(self, "h", None):
+            lib.moe_quant_destroy(self.h)
             self.h = None
 
     def __del__(self):

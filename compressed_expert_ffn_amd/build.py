@@ -19,7 +19,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libcefn.so")
-SOURCES = ["route.hip", "gemm.hip", "train.hip", "api.hip", "backward.hip", "offload.hip", "pack.cpp",
+SOURCES = ["route.hip", "gemm.hip", "train.hip", "quant.hip", "api.hip", "backward.hip", "offload.hip", "pack.cpp",
            "cluster.cpp"]
 ARCH = "gfx950"
 
