@@ -15,7 +15,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libcefn.so")
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_OOM, MOE_ERR_HIP = range(5)
-DTYPE = {"f32": 0, "f16": 1, "bf16": 2}
+DTYPE = {"f32": 0, "f16": 1, "bf16": 2, "int4_g32": 3}  # int4_g32: storage of the base only
 RESID = {"none": 0, "f32": 1, "f16": 2, "int4_g32": 3}
 ACT = {"gelu_tanh": 0, "swiglu": 1}
 
@@ -91,6 +91,7 @@ def _load():
         "moe_route": ([P, P, C.c_int32, C.POINTER(moe_route_out), P], C.c_int),
         "moe_forward": ([P, P, C.c_int32, P, C.POINTER(moe_route_out), P], C.c_int),
         "moe_forward_noalloc": ([P, P, C.c_int32, P, C.POINTER(moe_route_out), P], C.c_int),
+        "moe_forward_few": ([P, P, C.c_int32, P, C.POINTER(moe_route_out), P], C.c_int),
         "moe_destroy": ([P], C.c_int),
         "moe_backward": ([P, P, C.c_int32, P, P, C.POINTER(moe_grads), P], C.c_int),
         "moe_offload_enable": ([P, C.c_int32], C.c_int),
@@ -161,10 +162,15 @@ def _host_ptr(a, keep):
 
 
 def _device_ptr(a, keep):
-    """Copy a host array to a new device buffer (kept alive in ``keep``)."""
+    """A device tensor's buffer, or a copy of a host array in a new one (kept
+    alive in ``keep``)."""
     import torch
     if a is None:
         return None
+    if isinstance(a, torch.Tensor):
+        t = a.contiguous() if a.is_cuda else a.contiguous().cuda()
+        keep.append(t)
+        return t.data_ptr()
     a = np.ascontiguousarray(a)
     t = torch.from_numpy(a.view(np.uint8).reshape(-1).copy()).cuda()
     keep.append(t)
@@ -182,7 +188,8 @@ class Layer:
 
     inputs: the host arrays of one layer (X is not needed), in the layout
     include/moe.h documents; fp16 arrays as numpy float16, bf16 as uint16 bits.
-    on_device: hand the weights over as device buffers (copied there first).
+    on_device: hand the weights over as device buffers (torch tensors as they
+    are, host arrays copied there first).
     """
 
     def __init__(self, cfg: moe_config, inputs: dict, on_device: bool = False):
@@ -190,13 +197,17 @@ class Layer:
         ptr = _device_ptr if on_device else _host_ptr
         w = moe_weights()
         w.on_device = 1 if on_device else 0
-        w.W_grp = ptr(np.asarray(inputs["W_grp"], dtype=np.float32), keep)
-        w.W_exp = ptr(None if inputs.get("W_exp") is None
-                      else np.asarray(inputs["W_exp"], dtype=np.float32), keep)
-        w.group_bias = ptr(None if inputs.get("group_bias") is None
-                           else np.asarray(inputs["group_bias"], dtype=np.float32), keep)
-        w.expert_bias = ptr(None if inputs.get("expert_bias") is None
-                            else np.asarray(inputs["expert_bias"], dtype=np.float32), keep)
+        import torch
+
+        def f32(a):
+            if a is None:
+                return None
+            return a.float() if isinstance(a, torch.Tensor) and on_device else np.asarray(a, dtype=np.float32)
+
+        w.W_grp = ptr(f32(inputs["W_grp"]), keep)
+        w.W_exp = ptr(f32(inputs.get("W_exp")), keep)
+        w.group_bias = ptr(f32(inputs.get("group_bias")), keep)
+        w.expert_bias = ptr(f32(inputs.get("expert_bias")), keep)
         for p, b in enumerate(inputs["base"]):
             w.base[p] = ptr(b, keep)
         for p, a in enumerate(inputs.get("A") or []):
@@ -207,7 +218,7 @@ class Layer:
         self.E = cfg.G * cfg.K
         self.k = cfg.top_groups * cfg.top_experts
         h = C.c_void_p()
-        check(lib.moe_create(C.byref(cfg), C.byref(w), None, C.byref(h)))
+        check(lib.moe_create(C.byref(cfg), C.byref(w), _stream_ptr(None) if on_device else None, C.byref(h)))
         self.h = h
 
     # ----------------------------------------------------------------------
@@ -333,6 +344,21 @@ class Layer:
         rop = C.byref(ro) if route_bufs is not None else None
         check(lib.moe_forward_noalloc(self.h, C.c_void_p(X.data_ptr()), X.shape[0],
                                       C.c_void_p(Y.data_ptr()), rop, _stream_ptr(stream)))
+        return Y
+
+    def forward_few(self, X, Y=None, route_bufs=None, stream=None):
+        """moe_forward_few: the layer for up to 32 tokens."""
+        import torch
+        if X.dim() != 2 or X.shape[1] != self.cfg.d or X.dtype != self._torch_x_dtype() or not X.is_contiguous():
+            raise ValueError(f"X: expected contiguous {self._torch_x_dtype()} [T, {self.cfg.d}], got {X.dtype} "
+                             f"{tuple(X.shape)}")
+        if Y is None:
+            Y = torch.empty_like(X)
+        elif Y.shape != X.shape or Y.dtype != X.dtype or not Y.is_contiguous() or Y.device != X.device:
+            raise ValueError(f"Y: expected contiguous {X.dtype} {tuple(X.shape)} on {X.device}, got {Y.dtype} "
+                             f"{tuple(Y.shape)} on {Y.device}")
+        rop = None if route_bufs is None else C.byref(self._route_struct(route_bufs))
+        check(lib.moe_forward_few(self.h, X.data_ptr(), X.shape[0], Y.data_ptr(), rop, _stream_ptr(stream)))
         return Y
 
     def debug_residual(self, proj: int, which: int, expert: int):

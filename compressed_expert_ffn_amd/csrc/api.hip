@@ -26,6 +26,8 @@
 #include <vector>
 
 #include "api_internal.h"
+#include "few.h"
+#include "q4.h"
 
 using namespace cefn;
 using namespace cefn_api;
@@ -106,7 +108,7 @@ int validate(const moe_config* c) {
     return fail(MOE_ERR_INVALID_ARG, "config sizes must be positive (r >= 0, T_max >= 0)");
   if (c->act != MOE_ACT_GELU_TANH && c->act != MOE_ACT_SWIGLU)
     return fail(MOE_ERR_INVALID_ARG, "unknown activation %d", c->act);
-  if (c->x_dtype < 0 || c->x_dtype > 2 || c->base_dtype < 0 || c->base_dtype > 2)
+  if (c->x_dtype < 0 || c->x_dtype > 2 || c->base_dtype < 0 || c->base_dtype > 3)
     return fail(MOE_ERR_INVALID_ARG, "unknown dtype");
   if (c->resid < 0 || c->resid > 3) return fail(MOE_ERR_INVALID_ARG, "unknown residual kind");
   if (c->top_groups > c->G) return fail(MOE_ERR_INVALID_ARG, "top_groups %d > G %d", c->top_groups, c->G);
@@ -123,13 +125,14 @@ int validate(const moe_config* c) {
   if (c->r > 0 && c->K > 64) return fail(MOE_ERR_UNSUPPORTED, "residual experts need K <= 64");
   if (c->d % 64 || c->f % 64) return fail(MOE_ERR_UNSUPPORTED, "d and f must be multiples of 64");
   const int x = c->x_dtype, b = c->base_dtype;
-  const bool pair_ok = (x == MOE_F32 && b == MOE_F32) || (x == MOE_F16 && b == MOE_F16) ||
+  const bool q4 = b == MOE_INT4_G32;
+  const bool pair_ok = (q4 && x != MOE_F32) || (x == MOE_F32 && b == MOE_F32) || (x == MOE_F16 && b == MOE_F16) ||
                        (x == MOE_BF16 && b == MOE_BF16) || (x == MOE_BF16 && b == MOE_F16);
   if (!pair_ok) return fail(MOE_ERR_UNSUPPORTED, "unsupported (x, base) dtype pair (%d, %d)", x, b);
   if (c->resid == MOE_RESID_F32 && b != MOE_F32) return fail(MOE_ERR_UNSUPPORTED, "F32 residual needs an F32 base");
   if (c->resid == MOE_RESID_F16 && b != MOE_F16) return fail(MOE_ERR_UNSUPPORTED, "F16 residual needs an F16 base");
   if (c->resid == MOE_RESID_INT4_G32 && b == MOE_F32)
-    return fail(MOE_ERR_UNSUPPORTED, "INT4 residual needs an F16 or BF16 base");
+    return fail(MOE_ERR_UNSUPPORTED, "INT4 residual needs an F16, BF16 or INT4 base");
   return MOE_OK;
 }
 
@@ -153,7 +156,10 @@ void compute_stats(const moe_config& c, moe_stats_t* s) {
     dims(c, p, di, dn);
     params += (int64_t)c.G * di * dn + E * c.r * (int64_t)(di + dn);
     dense += E * (int64_t)di * dn;
-    bytes += (int64_t)c.G * di * dn * elem_bytes(c.base_dtype);
+    if (c.base_dtype == MOE_INT4_G32)
+      bytes += (int64_t)c.G * di * dn / 2 + (int64_t)c.G * (di / 32) * dn * 2;
+    else
+      bytes += (int64_t)c.G * di * dn * elem_bytes(c.base_dtype);
     if (c.resid == MOE_RESID_INT4_G32)
       bytes += E * ((int64_t)(di + dn) * c.r / 2 + (int64_t)(di + dn) / 32 * c.r * 2);
     else if (c.resid != MOE_RESID_NONE)
@@ -202,6 +208,7 @@ size_t carve_workspace(const moe_handle* h, long T, char* base, Workspace* ws) {
     }
     ws->L = reinterpret_cast<float*>(take(sizeof(float) * ((size_t)lmax * h->NCp + 4)));
   }
+  if (c.base_dtype == MOE_INT4_G32) return off;  // only moe_route uses this workspace
   if (c.r > 0) {
     ws->U = take(T * kg * h->NU * es + 16);
     ws->V = reinterpret_cast<float*>(take(sizeof(float) * (T * kg * h->NV + 4)));
@@ -236,42 +243,121 @@ int upload_raw(moe_handle* h, void** dst, const std::vector<T>& src) {
   return rc;
 }
 
+// Base weights in device memory, packed there: 16- and 32-bit ones in the same
+// order as pack_frag's, or quantised to 4 bits (q4.h; input projections in
+// tiles of 32 columns, 16 gate and 16 up for SwiGLU; output projection in
+// tiles of 16).  A host base (4-bit layers only) is sent over group by group.
+int build_base_on_device(moe_handle* h, const moe_weights* w, bool on_device) {
+  const moe_config& c = h->cfg;
+  const int G = c.G, P = h->P, Pin = h->P_in, d = c.d, f = c.f;
+  const bool q4 = c.base_dtype == MOE_INT4_G32;
+  const size_t es = q4 ? 4 : elem_bytes(c.base_dtype), mat = (size_t)d * f;
+  hipError_t e = hipSuccess;
+  if (!q4) {
+    char *w1 = nullptr, *w2 = nullptr;
+    h->w1_gs = (long)Pin * mat;
+    h->w2_gs = (long)mat;
+    TRY(dalloc(h, &w1, G * Pin * mat * es));
+    TRY(dalloc(h, &w2, G * mat * es));
+    h->W1 = w1;
+    h->W2 = w2;
+    h->weight_bytes += G * (Pin + 1) * mat * es;
+    e = launch_repack((int)es, w->base[0], Pin == 2 ? w->base[1] : nullptr, G, d, f, w1, nullptr);
+    if (e == hipSuccess) e = launch_repack((int)es, w->base[P - 1], nullptr, G, f, d, w2, nullptr);
+    if (e == hipSuccess) e = hipDeviceSynchronize();
+    return e == hipSuccess ? MOE_OK : hip_fail(h, e, "packing the base");
+  }
+  const Q4Shape s1{d, Pin * f, 2, 32}, s2{f, d, 1, 32};
+  uint32_t *w1 = nullptr, *w2 = nullptr;
+  h->w1_gs = s1.words();
+  h->w2_gs = s2.words();
+  h->w1_sgs = s1.scales();
+  h->w2_sgs = s2.scales();
+  TRY(dalloc(h, &w1, (size_t)G * s1.words()));
+  TRY(dalloc(h, &w2, (size_t)G * s2.words()));
+  TRY(dalloc(h, &h->W1_s, (size_t)G * s1.scales()));
+  TRY(dalloc(h, &h->W2_s, (size_t)G * s2.scales()));
+  h->W1 = w1;
+  h->W2 = w2;
+  h->weight_bytes += (size_t)G * ((s1.words() + s2.words()) * 4 + (s1.scales() + s2.scales()) * 2);
+  struct Staging {
+    void* p[3] = {};
+    ~Staging() {
+      for (void* q : p)
+        if (q) (void)hipFree(q);
+    }
+  } tmp;
+  if (!on_device)
+    for (int p = 0; p < P; ++p)
+      if (hipMalloc(&tmp.p[p], mat * es) != hipSuccess) {
+        (void)hipGetLastError();
+        return fail(MOE_ERR_OOM, "hipMalloc of %zu bytes failed", mat * es);
+      }
+  for (int g = 0; g < G && e == hipSuccess; ++g) {
+    const void* at[3] = {};
+    for (int p = 0; p < P && e == hipSuccess; ++p) {
+      const char* src = static_cast<const char*>(w->base[p]) + (size_t)g * mat * es;
+      at[p] = on_device ? src : tmp.p[p];
+      if (!on_device) e = hipMemcpy(tmp.p[p], src, mat * es, hipMemcpyHostToDevice);
+    }
+    Q4Source in{}, out{};
+    in.v[0] = at[0];
+    in.v[1] = Pin == 2 ? at[1] : nullptr;
+    in.v_dtype = out.v_dtype = MOE_F32;
+    in.n_src = Pin;
+    out.v[0] = at[P - 1];
+    out.n_src = 1;
+    if (e == hipSuccess)
+      e = launch_q4_pack(s1, in, h->mma, w1 + (size_t)g * s1.words(), h->W1_s + (size_t)g * s1.scales(), nullptr);
+    if (e == hipSuccess)
+      e = launch_q4_pack(s2, out, h->mma, w2 + (size_t)g * s2.words(), h->W2_s + (size_t)g * s2.scales(), nullptr);
+    if (e == hipSuccess && !on_device) e = hipDeviceSynchronize();  // before the staging buffers are reused
+  }
+  if (e == hipSuccess) e = hipDeviceSynchronize();
+  return e == hipSuccess ? MOE_OK : hip_fail(h, e, "packing the base");
+}
+
 // Build every device weight array.  TS is the storage type of the MFMA
 // dtype: float (F32) or uint16_t bits (F16/BF16), which is also the storage
-// type of the base and of F32/F16 residuals.
+// type of the base and of F32/F16 residuals.  base_on_device: w->base holds
+// device pointers, everything else host pointers.
 template <class TS>
-int build_weights(moe_handle* h, const moe_weights* w) {
+int build_weights(moe_handle* h, const moe_weights* w, bool base_on_device) {
   const moe_config& c = h->cfg;
   const int G = c.G, K = c.K, E = h->E, P = h->P, Pin = h->P_in, d = c.d, f = c.f, r = c.r;
   const bool swiglu = c.act == MOE_ACT_SWIGLU;
   auto base_ptr = [&](int p) { return static_cast<const TS*>(w->base[p]); };
 
-  // base input projections, gate/up interleaved in 32-column blocks for SwiGLU
-  {
-    const int N = Pin * f;
-    std::vector<TS> buf((size_t)G * N * d);
-    h->w1_gs = (long)N * d;
-    for (int g = 0; g < G; ++g) {
-      pack_frag(buf.data() + (size_t)g * N * d, N, d, true, [&](int n, int k) -> TS {
-        int p = 0, col = n;
-        if (swiglu) {
-          const int blk = n / 32;
-          p = blk & 1;
-          col = (blk >> 1) * 32 + (n & 31);
-        }
-        return base_ptr(p)[((size_t)g * d + k) * f + col];
-      });
+  if (base_on_device || c.base_dtype == MOE_INT4_G32) {
+    TRY(build_base_on_device(h, w, base_on_device));
+  } else {
+    // base input projections, gate/up interleaved in 32-column blocks for SwiGLU
+    {
+      const int N = Pin * f;
+      std::vector<TS> buf((size_t)G * N * d);
+      h->w1_gs = (long)N * d;
+      for (int g = 0; g < G; ++g) {
+        pack_frag(buf.data() + (size_t)g * N * d, N, d, true, [&](int n, int k) -> TS {
+          int p = 0, col = n;
+          if (swiglu) {
+            const int blk = n / 32;
+            p = blk & 1;
+            col = (blk >> 1) * 32 + (n & 31);
+          }
+          return base_ptr(p)[((size_t)g * d + k) * f + col];
+        });
+      }
+      TRY(upload_raw(h, &h->W1, buf));
     }
-    TRY(upload_raw(h, &h->W1, buf));
-  }
-  // base output projection [f][d]
-  {
-    std::vector<TS> buf((size_t)G * d * f);
-    h->w2_gs = (long)d * f;
-    for (int g = 0; g < G; ++g)
-      pack_frag(buf.data() + (size_t)g * d * f, d, f, true,
-                [&](int n, int k) -> TS { return base_ptr(P - 1)[((size_t)g * f + k) * d + n]; });
-    TRY(upload_raw(h, &h->W2, buf));
+    // base output projection [f][d]
+    {
+      std::vector<TS> buf((size_t)G * d * f);
+      h->w2_gs = (long)d * f;
+      for (int g = 0; g < G; ++g)
+        pack_frag(buf.data() + (size_t)g * d * f, d, f, true,
+                  [&](int n, int k) -> TS { return base_ptr(P - 1)[((size_t)g * f + k) * d + n]; });
+      TRY(upload_raw(h, &h->W2, buf));
+    }
   }
   if (r == 0) return MOE_OK;
 
@@ -542,9 +628,10 @@ int hip_fail(moe_handle* h, hipError_t e, const char* what) {
   return fail(MOE_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
 
-// Weights handed over as device pointers: read every array back into host
-// buffers (owned by `store`) and point a host-side copy of the struct at them,
-// so the packing below has one source form.
+// Weights handed over as device pointers: read the router and the residual
+// factors back into host buffers (owned by `store`) and point a host-side copy
+// of the struct at them, so the packing below has one source form.  The base,
+// nearly all of the bytes, stays where it is and is packed on the device.
 int weights_to_host(const moe_config& c, const moe_weights* w, moe_weights* hw,
                     std::vector<std::vector<char>>& store) {
   *hw = *w;
@@ -577,7 +664,12 @@ int weights_to_host(const moe_config& c, const moe_weights* w, moe_weights* hw,
   for (int p = 0; p < P; ++p) {
     int di, dn;
     dims(c, p, di, dn);
-    TRY(pull(w->base[p], (size_t)c.G * di * dn * elem_bytes(c.base_dtype), &hw->base[p]));
+    hipPointerAttribute_t at{};
+    if (w->base[p] && (hipPointerGetAttributes(&at, w->base[p]) != hipSuccess || at.type == hipMemoryTypeUnregistered)) {
+      (void)hipGetLastError();
+      return fail(MOE_ERR_INVALID_ARG, "on_device weights: base[%d] is not a device pointer", p);
+    }
+    hw->base[p] = w->base[p];
     if (c.r > 0) {
       TRY(pull(w->A[p], (size_t)E * di * c.r * rb, &hw->A[p]));
       TRY(pull(w->B[p], (size_t)E * dn * c.r * rb, &hw->B[p]));
@@ -681,7 +773,6 @@ int moe_config_stats(const moe_config* cfg, moe_stats_t* out) {
 }
 
 int moe_create(const moe_config* cfg, const moe_weights* wts, void* stream, moe_handle** out) {
-  (void)stream;
   TRY(validate(cfg));
   if (!wts || !out) return fail(MOE_ERR_INVALID_ARG, "null weights or output handle");
   *out = nullptr;
@@ -690,6 +781,11 @@ int moe_create(const moe_config* cfg, const moe_weights* wts, void* stream, moe_
   std::vector<std::vector<char>> host_store;
   const moe_weights* w = wts;
   if (wts->on_device) {
+    // work that writes the weights may still be on the caller's stream
+    if (hipStreamSynchronize(static_cast<hipStream_t>(stream)) != hipSuccess) {
+      (void)hipGetLastError();
+      return fail(MOE_ERR_HIP, "synchronising the weights' stream failed");
+    }
     TRY(weights_to_host(c, wts, &host_w, host_store));
     w = &host_w;
   }
@@ -706,7 +802,7 @@ int moe_create(const moe_config* cfg, const moe_weights* wts, void* stream, moe_
   h->k = c.top_groups * c.top_experts;
   h->P = P;
   h->P_in = P - 1;
-  h->mma = c.base_dtype;
+  h->mma = c.base_dtype == MOE_INT4_G32 ? c.x_dtype : c.base_dtype;
   h->NU = c.r > 0 ? (int)roundup((long)c.K * h->P_in * RPAD, 64) : 0;
   h->NV = c.r > 0 ? (int)roundup((long)c.K * RPAD, 64) : 0;
   if (hipGetDevice(&h->device) != hipSuccess) return fail(MOE_ERR_HIP, "no HIP device");
@@ -776,7 +872,9 @@ int moe_create(const moe_config* cfg, const moe_weights* wts, void* stream, moe_
       TRY(upload(h.get(), &h->ebias, eb));
     }
   }
-  int rc = (h->mma == MOE_F32) ? build_weights<float>(h.get(), w) : build_weights<uint16_t>(h.get(), w);
+  const bool dev_base = wts->on_device != 0;
+  int rc = (h->mma == MOE_F32) ? build_weights<float>(h.get(), w, dev_base)
+                               : build_weights<uint16_t>(h.get(), w, dev_base);
   if (rc) {
     moe_destroy(h.release());
     return rc;
@@ -792,6 +890,11 @@ int moe_create(const moe_config* cfg, const moe_weights* wts, void* stream, moe_
       return rc;
     }
     carve_workspace(h.get(), c.T_max, buf, &h->ws);
+  }
+  rc = create_few(h.get());
+  if (rc) {
+    moe_destroy(h.release());
+    return rc;
   }
   if (hipMemset(h->ws.cc, 0, sizeof(int) * ((size_t)h->ws.cc_n + 1)) != hipSuccess ||
       hipDeviceSynchronize() != hipSuccess) {
@@ -809,6 +912,7 @@ int moe_destroy(moe_handle* h) {
   for (hipEvent_t e : h->ev) (void)hipEventDestroy(e);
   delete_bwd(h);
   delete_offload(h);
+  delete h->few;
   delete h;
   return MOE_OK;
 }
@@ -1128,6 +1232,7 @@ int moe_forward(moe_handle* h, const void* X, int32_t T, void* Y, const moe_rout
   if (!X || !Y) return fail(MOE_ERR_INVALID_ARG, "null X or Y");
   if (X == Y) return fail(MOE_ERR_INVALID_ARG, "X and Y may not alias");
   if (h->off) return fail(MOE_ERR_UNSUPPORTED, "the handle's groups are offloaded: use moe_forward_offload");
+  if (c.base_dtype == MOE_INT4_G32) return fail(MOE_ERR_UNSUPPORTED, "a 4-bit base runs in moe_forward_few only");
   return forward_impl(h, h->ws, X, T, Y, routing, static_cast<hipStream_t>(stream));
 }
 
@@ -1140,6 +1245,7 @@ int moe_forward_noalloc(moe_handle* h, const void* X, int32_t T, void* Y, const 
   if (!X || !Y) return fail(MOE_ERR_INVALID_ARG, "null X or Y");
   if (X == Y) return fail(MOE_ERR_INVALID_ARG, "X and Y may not alias");
   if (h->off) return fail(MOE_ERR_UNSUPPORTED, "the handle's groups are offloaded: use moe_forward_offload");
+  if (c.base_dtype == MOE_INT4_G32) return fail(MOE_ERR_UNSUPPORTED, "a 4-bit base runs in moe_forward_few only");
   int dev = -1;
   if (hipGetDevice(&dev) != hipSuccess) return fail(MOE_ERR_HIP, "no HIP device");
   if (dev != h->device) return fail(MOE_ERR_INVALID_ARG, "handle lives on device %d, device %d is current", h->device, dev);

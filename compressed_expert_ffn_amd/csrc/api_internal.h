@@ -41,6 +41,16 @@ struct Workspace {
   float* ypart = nullptr;
 };
 
+// Workspace of moe_forward_few, for T_cap = min(T_max, 32) tokens.  The ticket
+// is zero between passes; the last row of H stays zero.
+struct FewState {
+  int T_cap = 0;
+  int *idx = nullptr, *gidx = nullptr, *glist = nullptr, *ticket = nullptr;
+  int16_t* grow = nullptr;
+  float *w = nullptr, *L = nullptr, *U = nullptr, *Vp = nullptr;
+  void* H = nullptr;
+};
+
 struct moe_handle {
   moe_config cfg{};
   int E = 0, k = 0, P = 0, P_in = 0, mma = 0, NU = 0, NV = 0;
@@ -53,6 +63,8 @@ struct moe_handle {
   float* L = nullptr;  // router scores (k-split partials)
   void *W1 = nullptr, *W2 = nullptr, *At = nullptr, *B1 = nullptr, *Ad = nullptr, *Bd = nullptr;
   uint16_t *At_s = nullptr, *B1_s = nullptr, *Ad_s = nullptr, *Bd_s = nullptr;
+  uint16_t *W1_s = nullptr, *W2_s = nullptr;  // scales of a 4-bit base
+  long w1_sgs = 0, w2_sgs = 0;
   long w1_gs = 0, w2_gs = 0, at_gs = 0, at_sgs = 0, bd_gs = 0;
   Workspace ws;         // the handle's own workspace, carved for T_max
   int nt1 = 0;          // column tiles of gemm1 (partials of V per row)
@@ -73,6 +85,7 @@ struct moe_handle {
   std::vector<hipEvent_t> ev;          // [prof_max][kStages][2]
   std::vector<unsigned char> ev_used;  // [prof_max][kStages]
   struct BwdState* bwd = nullptr;      // backward-pass layouts and workspace (built on first use)
+  FewState* few = nullptr;      // workspace of the few-token forward pass
   struct OffloadState* off = nullptr;  // idle-group offload (moe_offload_enable)
 };
 
@@ -157,6 +170,9 @@ int fwd_prelude(moe_handle* h, Workspace& ws, const void* X, int T, const moe_ro
 int fwd_gemms(moe_handle* h, Workspace& ws, const void* X, int T, void* Y, hipStream_t st, FwdState& fs,
               const int* gcounts, const int* gslot);
 int fwd_combine(moe_handle* h, Workspace& ws, int T, void* Y, hipStream_t st, FwdState& fs);
+
+// Allocate the workspace of moe_forward_few (few_api.hip).
+int create_few(moe_handle* h);
 
 // Release the backward / offload state of a handle (backward.hip, offload.hip).
 void delete_bwd(moe_handle* h);

@@ -264,6 +264,7 @@ int moe_backward(moe_handle* h, const void* X, int32_t T, const void* dY, void* 
       return fail(MOE_ERR_INVALID_ARG, "gradient buffer of projection %d is null", p);
   if (!gr->dW_grp) return fail(MOE_ERR_INVALID_ARG, "dW_grp is null");
   if (h->off) return fail(MOE_ERR_UNSUPPORTED, "the handle's groups are offloaded");
+  if (c.base_dtype == MOE_INT4_G32) return fail(MOE_ERR_UNSUPPORTED, "a 4-bit base has no backward pass");
   TRY(prepare_backward(h));
   BwdState* B = h->bwd;
   hipStream_t st = static_cast<hipStream_t>(stream);

@@ -1,0 +1,68 @@
+// Internal interface of the few-token forward pass (few.hip).
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "common.h"
+
+namespace cefn {
+
+constexpr int FEW_MAX_T = 32;   // tokens a pass takes: two 16-row MFMA tiles
+constexpr int FEW_WAVES = 16;   // wavefronts per workgroup of every kernel
+
+struct FewArgs {
+  const void* X;  // [T][d]
+  void* Y;        // [T][d]
+  int T, d, f, G, K, kg, ke, k, E, Pin;
+  int resid, act;
+  // router (layout in kernels.h)
+  const float* Wr;
+  int NCp, nsplit;
+  const float *gbias, *ebias;
+  float* L;       // [nsplit][T][NCp] partial scores
+  int* ticket;    // zero between passes
+  // routing results, and the caller's lists (null where not asked for)
+  int* idx;       // [T][k]
+  float* w;       // [T][k]
+  int* gidx;      // [T][kg]
+  int *counts, *offsets, *perm, *gcounts, *goffsets, *gperm;
+  // touched groups: glist[0] of them, glist[1 + a] the a-th (ascending), and
+  // grow[a][t] the row t*kg + rank of token t in it, or -1
+  int* glist;
+  int16_t* grow;  // [min(G, T*kg)][FEW_MAX_T]
+  // residual input factors
+  const void* At;
+  const uint16_t* At_s;
+  long at_gs, at_sgs;
+  int NU;
+  float* U;       // [T][E][Pin][16]
+  int u_all;      // U of every expert, in the scores' launch; 0: of the chosen ones, in a launch of its own
+  // weights (layouts in kernels.h; 4-bit bases in q4.h)
+  const void *W1, *W2;
+  long w1_gs, w2_gs;             // per group: elements, or 32-bit words of a 4-bit base
+  const uint16_t *W1_s, *W2_s;   // 4-bit base: scales
+  long w1_sgs, w2_sgs;
+  const void *B1, *Ad, *Bd;
+  long bd_gs;
+  int NV;
+  const uint16_t *B1_s, *Ad_s, *Bd_s;
+  float* Vp;      // [f blocks][T*k][16] partials of h A_down
+  void* H;        // [T*kg][planes][f]: gate-weighted hidden sums, fp32 (one plane), or two 16-bit planes, value and rest
+  int zero_row;   // row of H that stays zero (the last of the workspace)
+};
+
+// Columns of f per input-projection workgroup (32 weight columns).
+inline __host__ __device__ int few_fcols(int Pin) { return 32 / Pin; }
+// k splits of the score product over workgroups.
+int few_router_splits(int d);
+hipError_t launch_few_route(int xt, int ty, const FewArgs& a, hipStream_t st);
+hipError_t launch_few_up(int xt, int ty, bool q4, const FewArgs& a, hipStream_t st);
+hipError_t launch_few_down(int xt, int ty, bool q4, const FewArgs& a, hipStream_t st);
+
+// Base weights [rows n_in][cols] per group in device memory to the
+// fragment-major order of kernels.h; es: element bytes.  src1: the second of
+// two column-interleaved sources (SwiGLU's up projection) or null.
+hipError_t launch_repack(int es, const void* src0, const void* src1, int groups, int n_in, int n_out, void* dst,
+                         hipStream_t st);
+
+}  // namespace cefn

@@ -1,0 +1,996 @@
+// The whole layer for a few tokens (moe_forward_few): 1 to 32 rows.
+//
+// With so few rows the layer is a stream of weights: every byte of the
+// touched groups' bases is read once, for all tokens together, and the rows
+// sit in the registers as the 16 rows of a 16x16x32 MFMA operand (two tiles
+// beyond 16 tokens).  What is left to save is launches and latency, so the
+// pass has three kernels, each cut into workgroups of 16 columns of output
+// whose 16 wavefronts split the depth of the product:
+//   route  router scores; the last workgroup to finish them selects groups
+//          and experts for every token and lists the touched groups; beside
+//          it, u = x A for every expert where that is less than a launch
+//          (else for the chosen ones, in a launch of its own)
+//   up     z = x W1 of each touched group, then per (token, chosen expert)
+//          z + u B, the activation, the gate weight, the sum over the
+//          group's experts, and partials of h A_down over the columns
+//   down   y = sum over the touched groups of hbar W2, plus the residual
+//          tail (sum of the partials) B_down, for 16 columns of y
+// The rows of the up and down products belong to tokens; a token that did
+// not choose a group has a zero row in the down product, so the sum over
+// groups is the accumulator's own and no combine pass is left.
+//
+// Everything between the kernels is held in 32 bits, or as two 16-bit parts
+// of a 32-bit number where it feeds a 16-bit MFMA (the hidden sums), and
+// residual codes multiply as integers with their scale applied to the sum:
+// y is rounded once.
+#include "few.h"
+#include "kernels.h"
+#include "q4.h"
+#include "stream.h"
+#include "topk.h"
+
+namespace cefn {
+
+namespace {
+
+constexpr int NW = FEW_WAVES;
+constexpr int NT = NW * 64;
+
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+
+// Eight consecutive activations as loaded, and as operands.
+template <int XT>
+struct Raw {
+  u4v v[XT == DT_F32 ? 2 : 1];
+};
+template <int XT>
+__device__ __forceinline__ Raw<XT> load_raw(const typename Elem<XT>::T* p) {
+  Raw<XT> r;
+  r.v[0] = reinterpret_cast<const u4v*>(p)[0];
+  if constexpr (XT == DT_F32) r.v[1] = reinterpret_cast<const u4v*>(p)[1];
+  return r;
+}
+template <int XT>
+__device__ __forceinline__ void raw_to_f32(const Raw<XT>& r, float (&o)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    if constexpr (XT == DT_F32) {
+      const uint32_t u = r.v[e >> 2][e & 3];
+      o[e] = __uint_as_float(u);
+    } else {
+      const uint32_t u = r.v[0][e >> 1];
+      const uint16_t b = static_cast<uint16_t>((u >> (16 * (e & 1))) & 0xFFFFu);
+      o[e] = XT == DT_F16 ? f16_bits_to_f32(b) : bf16_bits_to_f32(b);
+    }
+  }
+}
+template <int XT, int TY>
+__device__ __forceinline__ typename Frag<TY>::T raw_to_frag(const Raw<XT>& r) {
+  if constexpr (XT == TY && TY != DT_F32) {
+    return __builtin_bit_cast(typename Frag<TY>::T, r.v[0]);
+  } else {
+    float v[8];
+    raw_to_f32<XT>(r, v);
+    return to_frag<TY>(v);
+  }
+}
+template <int TY>
+__device__ __forceinline__ void frag_to_f32(const typename Frag<TY>::T& f, float (&o)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) o[e] = static_cast<float>(f[e]);
+}
+
+// Eight values of a residual factor as fp32: stored floats, or the codes of
+// one word with a scale each (s) or one scale (s1).
+template <int TY>
+__device__ __forceinline__ void factor8(int resid, const void* base, long i8, const uint16_t* s, bool one_scale,
+                                        float (&o)[8]) {
+  if (resid == RS_INT4) {
+    const uint32_t w = static_cast<const uint32_t*>(base)[i8];
+    if (one_scale) {
+      const float sc = f16_bits_to_f32(*s);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = int4_value(w, e, sc);
+    } else {
+      const u4v sv = *reinterpret_cast<const u4v*>(s);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t u = sv[e >> 1];
+        o[e] = int4_value(w, e, f16_bits_to_f32(static_cast<uint16_t>((u >> (16 * (e & 1))) & 0xFFFFu)));
+      }
+    }
+    return;
+  }
+  constexpr int es = TY == DT_F32 ? 4 : 2;
+  frag_to_f32<TY>(load_frag<TY>(static_cast<const char*>(base) + i8 * 8 * es), o);
+}
+
+// ---------------------------------------------------------------- route --
+// Scores of 32 columns over this workgroup's part of the depth, in fp32
+// MFMAs (the router runs in FP32; the matrix is small and the MFMAs hide
+// behind its loads).
+template <int XT, int MT>
+__device__ void score_block(const FewArgs& a, int cb, int split, float* red) {
+  using XE = typename Elem<XT>::T;
+  const int wave = wave_id(), lane = threadIdx.x & 63, l = lane & 15, q = lane >> 4;
+  const int n32 = a.d / 32, part = split * NW + wave, parts = a.nsplit * NW;
+  const int u0 = static_cast<int>(static_cast<long>(n32) * part / parts);
+  const int u1 = static_cast<int>(static_cast<long>(n32) * (part + 1) / parts);
+  const XE* xp[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+    xp[m] = static_cast<const XE*>(a.X) + static_cast<long>(min(16 * m + l, a.T - 1)) * a.d + 8 * q;
+  // column cb*32 + 16 c + l, depth 8 q .. of each 32
+  const float* wp = a.Wr + (static_cast<long>(q >> 1) * a.NCp + cb * 32 + l) * 16 + 8 * (q & 1);
+  const long wstep = 2L * a.NCp * 16;
+  struct Slot {
+    Raw<XT> x[MT];
+    f8 w[2];
+  };
+  f4v acc[2][MT];
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[c][m] = f4v{0.f, 0.f, 0.f, 0.f};
+  stream_units<2, Slot>(
+      u1 - u0,
+      [&](int i, Slot& s) {
+        const long u = u0 + i;
+#pragma unroll
+        for (int m = 0; m < MT; ++m) s.x[m] = load_raw<XT>(xp[m] + u * 32);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) s.w[c] = load_frag<DT_F32>(wp + u * wstep + c * 256);
+      },
+      [&](const Slot& s) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const f8 x = raw_to_frag<XT, DT_F32>(s.x[m]);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) acc[c][m] = mfma16<DT_F32>(x, s.w[c], acc[c][m]);
+        }
+      });
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+      *reinterpret_cast<f4v*>(red + ((wave * 2 + c) * MT + m) * 256 + lane * 4) = acc[c][m];
+}
+
+// Sum over wavefronts of element (row, column) of a 32-column block left by
+// score_block or u_block.
+template <int MT>
+__device__ __forceinline__ float block_sum(const float* red, int row, int col) {
+  const int r = row & 15;
+  const int at = ((col >> 4) * MT + (row >> 4)) * 256 + (16 * (r >> 2) + (col & 15)) * 4 + (r & 3);
+  float s = 0.f;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) s += red[w * 2 * MT * 256 + at];
+  return s;
+}
+
+// u = x A for the 32 factor columns of block nb of group g.
+template <int XT, int TY, bool INT4, int MT>
+__device__ void u_block(const FewArgs& a, int g, int nb, float* red) {
+  using XE = typename Elem<XT>::T;
+  using B = typename Frag<TY>::T;
+  const int wave = wave_id(), lane = threadIdx.x & 63, l = lane & 15, q = lane >> 4;
+  const int n64 = a.d / 64;
+  const int u0 = n64 * wave / NW, u1 = n64 * (wave + 1) / NW;
+  const XE* xp[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+    xp[m] = static_cast<const XE*>(a.X) + static_cast<long>(min(16 * m + l, a.T - 1)) * a.d + 8 * q;
+  // fragment 4 u + q of the block, lane half h, columns 16 c + l: depth 64 u + 32 h + 8 q ..
+  const long at = (static_cast<long>(nb) * (a.d / 16) + q) * 64 + l;
+  f4v acc[2][MT];
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[c][m] = f4v{0.f, 0.f, 0.f, 0.f};
+  if constexpr (INT4) {
+    const uint32_t* wp = static_cast<const uint32_t*>(a.At) + g * a.at_gs + at;
+    const uint16_t* sp = a.At_s + g * a.at_sgs + static_cast<long>(nb) * (a.d / 32) * 32 + l;
+    struct Slot {
+      Raw<XT> x[2][MT];
+      uint32_t w[2][2];
+      uint16_t s[2][2];
+    };
+    stream_units<2, Slot>(
+        u1 - u0,
+        [&](int i, Slot& s) {
+          const long u = u0 + i;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m) s.x[h][m] = load_raw<XT>(xp[m] + u * 64 + 32 * h);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              s.w[h][c] = wp[u * 256 + 32 * h + 16 * c];
+              s.s[h][c] = sp[(2 * u + h) * 32 + 16 * c];
+            }
+          }
+        },
+        [&](const Slot& s) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            B x[MT];
+#pragma unroll
+            for (int m = 0; m < MT; ++m) x[m] = raw_to_frag<XT, TY>(s.x[h][m]);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const B b = int4_frag_1scale<TY>(s.w[h][c], 0x3C00);  // the codes themselves
+              const float sc = f16_bits_to_f32(s.s[h][c]);
+#pragma unroll
+              for (int m = 0; m < MT; ++m) {
+                const f4v p = mfma16<TY>(x[m], b, f4v{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[c][m][i] += sc * p[i];
+              }
+            }
+          }
+        });
+  } else {
+    constexpr int es = TY == DT_F32 ? 4 : 2;
+    const char* wp = static_cast<const char*>(a.At) + (g * a.at_gs + at * 8) * es;
+    struct Slot {
+      Raw<XT> x[2][MT];
+      B w[2][2];
+    };
+    stream_units<TY == DT_F32 ? 1 : 2, Slot>(
+        u1 - u0,
+        [&](int i, Slot& s) {
+          const long u = u0 + i;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m) s.x[h][m] = load_raw<XT>(xp[m] + u * 64 + 32 * h);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) s.w[h][c] = load_frag<TY>(wp + (u * 2048 + 256 * h + 128 * c) * es);
+          }
+        },
+        [&](const Slot& s) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+              const B x = raw_to_frag<XT, TY>(s.x[h][m]);
+#pragma unroll
+              for (int c = 0; c < 2; ++c) acc[c][m] = mfma16<TY>(x, s.w[h][c], acc[c][m]);
+            }
+        });
+  }
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+      *reinterpret_cast<f4v*>(red + ((wave * 2 + c) * MT + m) * 256 + lane * 4) = acc[c][m];
+  __syncthreads();
+  // column (j * Pin + p) * 16 + rho of the group
+  const int cols = a.K * a.Pin * 16;
+  for (int v = threadIdx.x; v < a.T * 32; v += NT) {
+    const int row = v >> 5, col = v & 31;
+    if (nb * 32 + col >= cols) continue;
+    a.U[(static_cast<long>(row) * a.G + g) * cols + nb * 32 + col] = block_sum<MT>(red, row, col);
+  }
+}
+
+// Selection for every token, the touched groups, and the caller's lists, by
+// one workgroup.  sc: [16][NC] scores of 16 tokens at a time.
+__device__ void select_all(const FewArgs& a, float* sc, int* sidx, int* sgid, int* cnt) {
+  const int tid = threadIdx.x, wave = wave_id(), lane = tid & 63;
+  const int NC = a.G + (a.K > 1 ? a.G * a.K : 0);
+  for (int t0 = 0; t0 < a.T; t0 += NW) {
+    const int nt = min(NW, a.T - t0);
+    for (int e = tid; e < nt * NC; e += NT) {
+      const int tk = e / NC, c = e - tk * NC;
+      const float* p = a.L + static_cast<long>(t0 + tk) * a.NCp + c;
+      const long stride = static_cast<long>(a.T) * a.NCp;
+      float part[8];
+#pragma unroll
+      for (int s = 0; s < 8; ++s)
+        part[s] = s < a.nsplit ? __hip_atomic_load(p + s * stride, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0.f;
+      float v = ((part[0] + part[1]) + (part[2] + part[3])) + ((part[4] + part[5]) + (part[6] + part[7]));
+      if (c < a.G) {
+        if (a.gbias) v += a.gbias[c];
+      } else if (a.ebias) {
+        v += a.ebias[c - a.G];
+      }
+      sc[e] = v;
+    }
+    __syncthreads();
+    if (wave < nt) {
+      // gates: softmax over the chosen groups times softmax over the chosen
+      // experts of each
+      const int t = t0 + wave;
+      const float* st = sc + wave * NC;
+      float gvl, evl;
+      int gil, eil;
+      wave_topk(st, a.G, a.kg, lane, gvl, gil);
+      const float g0 = __shfl(gvl, 0);
+      float ps = 0.f;
+      for (int i = 0; i < a.kg; ++i) ps += expf(__shfl(gvl, i) - g0);
+      for (int ga = 0; ga < a.kg; ++ga) {
+        const int g = __shfl(gil, ga);
+        const float pg = expf(__shfl(gvl, ga) - g0) / ps;
+        if (a.K == 1) {
+          if (lane == 0) {
+            sidx[t * a.k + ga] = g;
+            a.idx[t * a.k + ga] = g;
+            a.w[t * a.k + ga] = pg;
+          }
+        } else {
+          wave_topk(st + a.G + g * a.K, a.K, a.ke, lane, evl, eil);
+          const float e0 = __shfl(evl, 0);
+          float qs = 0.f;
+          for (int b = 0; b < a.ke; ++b) qs += expf(__shfl(evl, b) - e0);
+          if (lane < a.ke) {
+            const int slot = t * a.k + ga * a.ke + lane;
+            sidx[slot] = g * a.K + eil;
+            a.idx[slot] = g * a.K + eil;
+            a.w[slot] = pg * (expf(evl - e0) / qs);
+          }
+        }
+        if (lane == 0) {
+          sgid[t * a.kg + ga] = g;
+          a.gidx[t * a.kg + ga] = g;
+        }
+      }
+    }
+    __syncthreads();
+  }
+  // tokens per group, then the touched groups in ascending order
+  const int ng = a.T * a.kg, na = a.T * a.k;
+  if (tid < a.G) {
+    int n = 0;
+    for (int i = 0; i < ng; ++i) n += sgid[i] == tid ? 1 : 0;
+    cnt[tid] = n;
+  }
+  __syncthreads();
+  if (tid < a.G) {
+    int at = 0, before = 0;
+    for (int g = 0; g < tid; ++g) {
+      at += cnt[g] > 0 ? 1 : 0;
+      before += cnt[g];
+    }
+    if (cnt[tid] > 0) {
+      a.glist[1 + at] = tid;
+      for (int t = 0; t < a.T; ++t) {
+        int row = -1;
+        for (int r = 0; r < a.kg; ++r)
+          if (sgid[t * a.kg + r] == tid) row = t * a.kg + r;
+        a.grow[at * FEW_MAX_T + t] = static_cast<int16_t>(row);
+      }
+    }
+    if (tid == a.G - 1) a.glist[0] = at + (cnt[tid] > 0 ? 1 : 0);
+    if (a.gcounts) a.gcounts[tid] = cnt[tid];
+    if (a.goffsets) {
+      a.goffsets[tid] = before;
+      if (tid == a.G - 1) a.goffsets[a.G] = ng;
+    }
+  }
+  // an entry's place in its bin's list: the entries of lower bins, and those
+  // before it in its own (tokens ascend within a bin)
+  if (a.gperm && tid < ng) {
+    int at = 0;
+    for (int i = 0; i < ng; ++i) at += (sgid[i] < sgid[tid] || (sgid[i] == sgid[tid] && i < tid)) ? 1 : 0;
+    a.gperm[at] = tid / a.kg;
+  }
+  if (a.perm && tid < na) {
+    int at = 0;
+    for (int i = 0; i < na; ++i) at += (sidx[i] < sidx[tid] || (sidx[i] == sidx[tid] && i < tid)) ? 1 : 0;
+    a.perm[at] = tid / a.k;
+  }
+  if (a.counts || a.offsets) {
+    for (int e = tid; e < a.E; e += NT) {
+      int n = 0, before = 0;
+      for (int i = 0; i < na; ++i) {
+        n += sidx[i] == e ? 1 : 0;
+        before += sidx[i] < e ? 1 : 0;
+      }
+      if (a.counts) a.counts[e] = n;
+      if (a.offsets) {
+        a.offsets[e] = before;
+        if (e == a.E - 1) a.offsets[a.E] = na;
+      }
+    }
+  }
+}
+
+// grid: the score blocks (32 columns x nsplit depth parts) first, then with
+// u_all one workgroup per 32 factor columns of every group.
+template <int XT, int TY, int RS, int MT>
+__global__ __launch_bounds__(NT) void few_route_kernel(FewArgs a) {
+  extern __shared__ __attribute__((aligned(16))) float red[];
+  __shared__ int sidx[FEW_MAX_T * MAX_SLOTS], sgid[FEW_MAX_T * MAX_KG], cnt[256];
+  __shared__ int last;
+  const int ncb = a.NCp / 32, nsb = ncb * a.nsplit;
+  if (static_cast<int>(blockIdx.x) >= nsb) {
+    if constexpr (RS != RS_NONE) {
+      const int ub = blockIdx.x - nsb, nbu = (a.K * a.Pin * 16 + 31) / 32;
+      u_block<XT, TY, RS == RS_INT4, MT>(a, ub / nbu, ub % nbu, red);
+    }
+    return;
+  }
+  const int cb = blockIdx.x % ncb, split = blockIdx.x / ncb;
+  score_block<XT, MT>(a, cb, split, red);
+  __syncthreads();
+  for (int v = threadIdx.x; v < a.T * 32; v += NT) {
+    const int row = v >> 5, col = v & 31;
+    __hip_atomic_store(a.L + (static_cast<long>(split) * a.T + row) * a.NCp + cb * 32 + col,
+                       block_sum<MT>(red, row, col), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  // the last workgroup to have stored its scores selects; nobody waits
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const int n = __hip_atomic_fetch_add(a.ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+    last = n == nsb - 1 ? 1 : 0;
+    if (last) __hip_atomic_store(a.ticket, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);  // for the next pass
+  }
+  __syncthreads();
+  if (!last) return;
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+  select_all(a, red, sidx, sgid, cnt);
+}
+
+// U of the chosen experts only: one workgroup per 32 factor columns, idle
+// where none of the columns' experts is chosen.
+template <int XT, int TY, int RS, int MT>
+__global__ __launch_bounds__(NT) void few_u_kernel(FewArgs a) {
+  extern __shared__ __attribute__((aligned(16))) float red[];
+  __shared__ int hit;
+  const int nbu = (a.K * a.Pin * 16 + 31) / 32;
+  const int g = blockIdx.x / nbu, nb = blockIdx.x % nbu;
+  const int per = 2 / a.Pin;  // experts per block
+  if (threadIdx.x == 0) hit = 0;
+  __syncthreads();
+  if (static_cast<int>(threadIdx.x) < a.T * a.k) {
+    const int e = a.idx[threadIdx.x] - (g * a.K + nb * per);
+    if (e >= 0 && e < per) hit = 1;
+  }
+  __syncthreads();
+  if (!hit) return;
+  u_block<XT, TY, RS == RS_INT4, MT>(a, g, nb, red);
+}
+
+// ------------------------------------------------------------------- up --
+// grid: (touched group a) x (blocks of FT = 32 / Pin columns of f).  A
+// workgroup's 32 weight columns are 16 of the gate and the same 16 of the up
+// projection (SwiGLU), or 32 of the one input projection (GELU).
+template <int XT, int TY, bool Q4, int MT>
+__global__ __launch_bounds__(NT) void few_up_kernel(FewArgs a) {
+  using XE = typename Elem<XT>::T;
+  using B = typename Frag<TY>::T;
+  extern __shared__ __attribute__((aligned(16))) float red[];  // partial tiles, then hw [rows][ke][FT]
+  __shared__ float z[2][MT * 16][16];
+  __shared__ int srow[FEW_MAX_T];   // (token << 16) | row t*kg + rank, of the group's tokens
+  __shared__ int nrows;
+  const int Pin = a.Pin, FT = 32 / Pin, nfb = a.f / FT;
+  const int ga = blockIdx.x / nfb, fb = blockIdx.x % nfb;
+  if (ga >= a.glist[0]) return;
+  const int g = a.glist[1 + ga];
+  const int wave = wave_id(), lane = threadIdx.x & 63, l = lane & 15, q = lane >> 4;
+  if (wave == 0) {
+    const int row = lane < a.T ? a.grow[ga * FEW_MAX_T + lane] : -1;
+    const unsigned long long m = __ballot(row >= 0);
+    if (row >= 0) srow[__popcll(m & ((1ull << lane) - 1))] = (lane << 16) | row;
+    if (lane == 0) nrows = __popcll(m);
+  }
+  const int n64 = a.d / 64;
+  const int u0 = n64 * wave / NW, u1 = n64 * (wave + 1) / NW;
+  const XE* xp[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+    xp[m] = static_cast<const XE*>(a.X) + static_cast<long>(min(16 * m + l, a.T - 1)) * a.d + 8 * q;
+  f4v acc[2][MT];
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[c][m] = f4v{0.f, 0.f, 0.f, 0.f};
+  if constexpr (Q4) {
+    const uint32_t* wp =
+        static_cast<const uint32_t*>(a.W1) + g * a.w1_gs + (static_cast<long>(fb) * n64 * 64 + lane) * 4;
+    const uint16_t* sp = a.W1_s + g * a.w1_sgs + (static_cast<long>(fb) * n64 * 16 + l) * 4;
+    struct Slot {
+      Raw<XT> x[2][MT];
+      u4v w;
+      u2v s;
+    };
+    const B ones = q4_ones<TY>();
+    stream_units<MT == 1 ? 4 : 2, Slot>(
+        u1 - u0,
+        [&](int i, Slot& s) {
+          const long u = u0 + i;
+          s.w = *reinterpret_cast<const u4v*>(wp + u * 256);
+          s.s = load_scales<4>(sp + u * 64);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int m = 0; m < MT; ++m) s.x[h][m] = load_raw<XT>(xp[m] + u * 64 + 32 * h);
+        },
+        [&](const Slot& s) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            f4v off[MT];
+            B x[MT];
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+              x[m] = raw_to_frag<XT, TY>(s.x[h][m]);
+              const f4v sum = mfma16<TY>(x[m], ones, f4v{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+              for (int i = 0; i < 4; ++i) off[m][i] = -kQ4Offset * sum[i];
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const uint32_t word = s.w[2 * h + c];
+              const B b = q4_frag<TY>(word);
+              const float sc = scale_at(s.s, 2 * h + c);
+#pragma unroll
+              for (int m = 0; m < MT; ++m) {
+                const f4v p = mfma16<TY>(x[m], b, off[m]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[c][m][i] += sc * p[i];
+              }
+            }
+          }
+        });
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[c][m][i] *= Q4Type<TY>::undo;
+  } else {
+    constexpr int es = TY == DT_F32 ? 4 : 2;
+    const char* wp[2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int n32 = Pin == 2 ? (fb & ~1) + c : fb, half = Pin == 2 ? fb & 1 : c;
+      wp[c] = static_cast<const char*>(a.W1) +
+              (g * a.w1_gs + ((static_cast<long>(n32) * (a.d / 16) + q) * 64 + 16 * half + l) * 8) * es;
+    }
+    struct Slot {
+      Raw<XT> x[2][MT];
+      B w[2][2];
+    };
+    stream_units<TY == DT_F32 ? 1 : MT == 1 ? 3 : 2, Slot>(
+        u1 - u0,
+        [&](int i, Slot& s) {
+          const long u = u0 + i;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) s.w[h][c] = load_frag<TY>(wp[c] + (u * 2048 + 256 * h) * es);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) s.x[h][m] = load_raw<XT>(xp[m] + u * 64 + 32 * h);
+          }
+        },
+        [&](const Slot& s) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+              const B x = raw_to_frag<XT, TY>(s.x[h][m]);
+#pragma unroll
+              for (int c = 0; c < 2; ++c) acc[c][m] = mfma16<TY>(x, s.w[h][c], acc[c][m]);
+            }
+        });
+  }
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+      *reinterpret_cast<f4v*>(red + ((wave * 2 + c) * MT + m) * 256 + lane * 4) = acc[c][m];
+  __syncthreads();
+  for (int v = threadIdx.x; v < MT * 16 * 32; v += NT) {
+    const int row = v >> 5, col = v & 31;
+    z[col >> 4][row][col & 15] = block_sum<MT>(red, row, col);
+  }
+  __syncthreads();  // partial tiles are read: red becomes hw
+  float* hw = red;
+  const int f0 = fb * FT, n = nrows;
+  for (int v = threadIdx.x; v < n * a.ke * FT; v += NT) {
+    const int c = v % FT, b = (v / FT) % a.ke, i = v / (FT * a.ke);
+    const int t = srow[i] >> 16, row = srow[i] & 0xFFFF;
+    const int slot = t * a.k + (row - t * a.kg) * a.ke + b;
+    const int e = a.idx[slot];
+    const float wgt = a.w[slot];
+    float zz[2];
+    zz[0] = Pin == 2 ? z[0][t][c] : z[c >> 4][t][c & 15];
+    zz[1] = Pin == 2 ? z[1][t][c] : 0.f;
+    if (a.resid != RS_NONE) {
+      const int col = f0 + c, n32 = col >> 5, nl = col & 31;
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        if (p >= Pin) break;
+        const float* u = a.U + (static_cast<long>(t) * a.E + e) * Pin * 16 + p * 16;
+        const long blk = static_cast<long>(e * Pin + p) * (a.f / 32) + n32;
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          float bv[8];
+          factor8<TY>(a.resid, a.B1, blk * 64 + 32 * hh + nl, a.B1_s + blk * RPAD + 8 * hh, false, bv);
+#pragma unroll
+          for (int r = 0; r < 8; ++r) zz[p] = fmaf(u[8 * hh + r], bv[r], zz[p]);
+        }
+      }
+    }
+    const float h = a.act == ACT_SWIGLU ? silu_f(zz[0]) * zz[1] : gelu_tanh_f(zz[0]);
+    hw[v] = wgt * h;
+  }
+  __syncthreads();
+  constexpr int planes = TY == DT_F32 ? 1 : 2;
+  for (int v = threadIdx.x; v < n * FT; v += NT) {
+    const int c = v % FT, i = v / FT;
+    const int row = srow[i] & 0xFFFF;
+    float s = 0.f;
+    for (int b = 0; b < a.ke; ++b) s += hw[(i * a.ke + b) * FT + c];
+    const long at = static_cast<long>(row) * planes * a.f + f0 + c;
+    if constexpr (TY == DT_F32) {
+      static_cast<float*>(a.H)[at] = s;
+    } else {
+      // two 16-bit parts: the rounded value and what it leaves
+      const uint16_t hi = from_f32<TY>(s);
+      const float back = TY == DT_F16 ? f16_bits_to_f32(hi) : bf16_bits_to_f32(hi);
+      static_cast<uint16_t*>(a.H)[at] = hi;
+      static_cast<uint16_t*>(a.H)[at + a.f] = from_f32<TY>(s - back);
+    }
+  }
+  if (a.resid != RS_NONE) {
+    const int f32 = f0 >> 5, st0 = (f0 >> 4) & 1;
+    for (int v = threadIdx.x; v < n * a.ke * 16; v += NT) {
+      const int rho = v & 15, ib = v >> 4, i = ib / a.ke, b = ib - i * a.ke;
+      const int t = srow[i] >> 16, row = srow[i] & 0xFFFF;
+      const int slot = t * a.k + (row - t * a.kg) * a.ke + b;
+      const int e = a.idx[slot];
+      const float* hp = hw + ib * FT;
+      const long blk = static_cast<long>(e) * (a.f / 32) + f32;
+      float s = 0.f;
+      for (int j = 0; j < FT / 16; ++j) {
+        const int st = st0 + j;
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          float av[8];
+          factor8<TY>(a.resid, a.Ad, (blk * 2 + st) * 64 + rho + 32 * hh, a.Ad_s + blk * RPAD + rho, true, av);
+#pragma unroll
+          for (int x = 0; x < 8; ++x) s = fmaf(hp[16 * j + 4 * hh + (x < 4 ? x : x + 4)], av[x], s);
+        }
+      }
+      a.Vp[(static_cast<long>(fb) * a.T * a.k + slot) * 16 + rho] = s;
+    }
+  }
+}
+
+// ----------------------------------------------------------------- down --
+// grid: one workgroup per 16 columns of y.  Its wavefronts take consecutive
+// ranges of the touched groups' depths, laid end to end.  MFMA rows: with
+// 32-bit MFMAs token 16 m + r of tile m; with 16-bit ones the two parts of
+// the hidden sums are rows of their own: up to 8 tokens share one tile
+// (parts in rows 0-7 and 8-15), else tile m holds part m / (MT / 2) of
+// tokens 16 (m % (MT / 2)) + r.
+template <int XT, int TY, bool Q4, int MT>
+__global__ __launch_bounds__(NT) void few_down_kernel(FewArgs a) {
+  using B = typename Frag<TY>::T;
+  extern __shared__ __attribute__((aligned(16))) float red[];  // [NW][MT][256], then V, tail, grow
+  const int n = blockIdx.x, nv = a.resid != RS_NONE ? a.T * a.k * 16 : 0;
+  float* V = red + NW * MT * 256;
+  float* tail = V + nv;
+  int16_t* grow = reinterpret_cast<int16_t*>(tail + max(nv, NT));
+  const int ng = a.glist[0];
+  const int tid = threadIdx.x, wave = wave_id(), lane = tid & 63, l = lane & 15, q = lane >> 4;
+  for (int i = tid; i < ng * FEW_MAX_T; i += NT) grow[i] = a.grow[i];
+  if (nv) {
+    // V: the partials summed over the blocks of f, in an order set by T, k and f alone
+    const int nfb = a.f * a.Pin / 32;
+    if (nv <= NT) {
+      const int parts = NT / nv, p = tid / nv, o = tid - p * nv;
+      float s = 0.f;
+      if (p < parts)
+        for (int b = p; b < nfb; b += parts) s += a.Vp[static_cast<long>(b) * nv + o];
+      if (p < parts) tail[tid] = s;
+      __syncthreads();
+      if (tid < nv) {
+        float v = 0.f;
+        for (int i = 0; i < parts; ++i) v += tail[i * nv + tid];
+        V[tid] = v;
+      }
+    } else {
+      for (int o = tid; o < nv; o += NT) {
+        float s = 0.f;
+#pragma unroll 8
+        for (int b = 0; b < nfb; ++b) s += a.Vp[static_cast<long>(b) * nv + o];
+        V[o] = s;
+      }
+    }
+  }
+  __syncthreads();
+  constexpr int planes = TY == DT_F32 ? 1 : 2;
+  constexpr int UNIT = Q4 ? 128 : 64, NS = UNIT / 32;
+  constexpr bool packed = planes == 2 && MT == 1;
+  const int nf = (a.f + UNIT - 1) / UNIT;
+  const int units = ng * nf;
+  const int u0 = static_cast<int>(static_cast<long>(units) * wave / NW);
+  const int u1 = static_cast<int>(static_cast<long>(units) * (wave + 1) / NW);
+  f4v acc[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) acc[m] = f4v{0.f, 0.f, 0.f, 0.f};
+  // the stream's place: group ordinal, unit inside it, the lane's rows
+  int at_i = 0, ga = u0 / nf, kb = u0 - ga * nf;
+  using HE = typename Elem<TY>::T;
+  const HE* hp[MT];
+  const char* wp = nullptr;
+  const uint16_t* sp = nullptr;
+  constexpr int es = TY == DT_F32 ? 4 : 2;
+  auto enter = [&]() {
+    const int g = a.glist[1 + ga];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const int t = packed ? (l & 7) : planes == 1 ? 16 * m + l : 16 * (m % (MT > 1 ? MT / 2 : 1)) + l;
+      const int plane = packed ? l >> 3 : planes == 1 ? 0 : m / (MT > 1 ? MT / 2 : 1);
+      const int row = t < a.T ? grow[ga * FEW_MAX_T + t] : -1;
+      // a token that did not choose the group reads the row of zeros
+      hp[m] = static_cast<const HE*>(a.H) + (static_cast<long>(row < 0 ? a.zero_row : row) * planes + plane) * a.f;
+    }
+    if constexpr (Q4) {
+      wp = reinterpret_cast<const char*>(static_cast<const uint32_t*>(a.W2) + g * a.w2_gs +
+                                         (static_cast<long>(n) * nf * 64 + lane) * 4);
+      sp = a.W2_s + g * a.w2_sgs + (static_cast<long>(n) * nf * 16 + l) * 4;
+    } else {
+      wp = static_cast<const char*>(a.W2) +
+           (g * a.w2_gs + ((static_cast<long>(n >> 1) * (a.f / 16) + q) * 64 + 16 * (n & 1) + l) * 8) * es;
+    }
+  };
+  if (u0 < u1) enter();
+  auto seek = [&](int i) {  // i is at_i or at_i + 1
+    if (i == at_i) return;
+    at_i = i;
+    if (++kb == nf) {
+      kb = 0;
+      ++ga;
+      enter();
+    }
+  };
+  if constexpr (Q4) {
+    struct Slot {
+      Raw<TY> x[NS][MT];
+      u4v w;
+      u2v s;
+    };
+    const B ones = q4_ones<TY>();
+    stream_units<MT == 1 ? 2 : 1, Slot>(
+        u1 - u0,
+        [&](int i, Slot& s) {
+          seek(i);
+          s.w = *reinterpret_cast<const u4v*>(wp + static_cast<long>(kb) * 1024);
+          s.s = load_scales<4>(sp + static_cast<long>(kb) * 64);
+#pragma unroll
+          for (int st = 0; st < NS; ++st) {
+            // depths past f repeat the row's last ones (their codes are zero)
+            const int k = min(kb * UNIT + 32 * st + 8 * q, a.f - 8);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) s.x[st][m] = load_raw<TY>(hp[m] + k);
+          }
+        },
+        [&](const Slot& s) {
+#pragma unroll
+          for (int st = 0; st < NS; ++st) {
+            const uint32_t word = s.w[st];
+            const B b = q4_frag<TY>(word);
+            const float sc = scale_at(s.s, st);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+              const B x = raw_to_frag<TY, TY>(s.x[st][m]);
+              const f4v sum = mfma16<TY>(x, ones, f4v{0.f, 0.f, 0.f, 0.f});
+              f4v off;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) off[i] = -kQ4Offset * sum[i];
+              const f4v p = mfma16<TY>(x, b, off);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) acc[m][i] += sc * p[i];
+            }
+          }
+        });
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[m][i] *= Q4Type<TY>::undo;
+  } else {
+    struct Slot {
+      Raw<TY> x[2][MT];
+      B w[2];
+    };
+    stream_units<TY == DT_F32 ? 2 : MT == 1 ? 4 : MT == 2 ? 3 : 2, Slot>(
+        u1 - u0,
+        [&](int i, Slot& s) {
+          seek(i);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            s.w[h] = load_frag<TY>(wp + (static_cast<long>(kb) * 2048 + 256 * h) * es);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) s.x[h][m] = load_raw<TY>(hp[m] + kb * 64 + 32 * h + 8 * q);
+          }
+        },
+        [&](const Slot& s) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int m = 0; m < MT; ++m) acc[m] = mfma16<TY>(raw_to_frag<TY, TY>(s.x[h][m]), s.w[h], acc[m]);
+        });
+  }
+#pragma unroll
+  for (int m = 0; m < MT; ++m) *reinterpret_cast<f4v*>(red + (wave * MT + m) * 256 + lane * 4) = acc[m];
+  // residual tail: (token, slot) times 16 columns
+  for (int v = tid; v < nv; v += NT) {
+    const int c = v & 15, slot = v >> 4, e = a.idx[slot];
+    const int g = e / a.K, j = e - g * a.K, n32 = n >> 1, nl = 16 * (n & 1) + c;
+    const long sblk = (static_cast<long>(e) * (a.d / 32) + n32) * RPAD;
+    const long base = a.resid == RS_INT4 ? g * a.bd_gs : g * a.bd_gs / 8;  // in eights of values
+    float s = 0.f;
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh) {
+      // rank column 8 hh .. of expert j in the permuted depth order
+      const int ks = 4 * (j >> 2) + 2 * (j & 1) + hh, half = (j >> 1) & 1;
+      float bv[8];
+      factor8<TY>(a.resid, a.Bd, base + (static_cast<long>(n32) * (a.NV / 16) + ks) * 64 + nl + 32 * half,
+                  a.Bd_s + sblk + 8 * hh, false, bv);
+#pragma unroll
+      for (int r = 0; r < 8; ++r) s = fmaf(V[slot * 16 + 8 * hh + r], bv[r], s);
+    }
+    tail[v] = s;
+  }
+  __syncthreads();
+  for (int v = tid; v < a.T * 16; v += NT) {
+    const int t = v >> 4, c = v & 15;
+    float s = 0.f;
+#pragma unroll
+    for (int p = planes - 1; p >= 0; --p) {  // the rests first
+      const int m = packed ? 0 : planes == 1 ? t >> 4 : p * (MT / 2) + (t >> 4);
+      const int r = packed ? t + 8 * p : t & 15;
+      const int at = m * 256 + (16 * (r >> 2) + c) * 4 + (r & 3);
+#pragma unroll
+      for (int w = 0; w < NW; ++w) s += red[w * MT * 256 + at];
+    }
+    if (nv)
+      for (int i = 0; i < a.k; ++i) s += tail[(t * a.k + i) * 16 + c];
+    static_cast<typename Elem<XT>::T*>(a.Y)[static_cast<long>(t) * a.d + n * 16 + c] = from_f32<XT>(s);
+  }
+}
+
+// --------------------------------------------------------------- repack --
+// One thread per fragment lane: 8 values of one column, the order of pack.h's
+// pack_frag with the permuted depth; two sources interleave in 32-column blocks.
+template <class TS>
+__global__ __launch_bounds__(256) void repack_kernel(const TS* src0, const TS* src1, int n_in, int n_out, TS* dst,
+                                                     long per_group) {
+  const long id = static_cast<long>(blockIdx.x) * 256 + threadIdx.x;
+  if (id >= per_group) return;
+  const int g = blockIdx.y, KS = n_in / 16;
+  const int lane = id & 63;
+  const long fr = id >> 6;
+  const int ks = static_cast<int>(fr % KS), nb = static_cast<int>(fr / KS);
+  const TS* src = src0;
+  int col = nb * 32 + (lane & 31);
+  if (src1) {
+    if (nb & 1) src = src1;
+    col = (nb >> 1) * 32 + (lane & 31);
+  }
+  src += static_cast<long>(g) * n_in * n_out;
+  const int k0 = 64 * (ks >> 2) + 32 * (lane >> 5) + 8 * (ks & 3);
+  TS* o = dst + (g * per_group + id) * 8;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) o[e] = src[static_cast<long>(k0 + e) * n_out + col];
+}
+
+// -------------------------------------------------------------- launches --
+template <class K>
+hipError_t go(K kernel, unsigned grid, size_t lds, const FewArgs& a, hipStream_t st) {
+  if (lds > 64 * 1024) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(lds));
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(kernel, dim3(grid), dim3(NT), lds, st, a);
+  return hipGetLastError();
+}
+
+template <int XT, int TY, int RS, int MT>
+hipError_t route_mt(const FewArgs& a, hipStream_t st) {
+  const unsigned nsb = (a.NCp / 32) * a.nsplit, nub = a.G * ((a.K * a.Pin * 16 + 31) / 32);
+  const size_t tiles = static_cast<size_t>(NW) * 2 * MT * 256 * sizeof(float);
+  const size_t sc = static_cast<size_t>(NW) * (a.G + (a.K > 1 ? a.G * a.K : 0)) * sizeof(float);
+  hipError_t e = go(few_route_kernel<XT, TY, RS, MT>, nsb + (RS != RS_NONE && a.u_all ? nub : 0),
+                    sc > tiles ? sc : tiles, a, st);
+  if constexpr (RS != RS_NONE)
+    if (e == hipSuccess && !a.u_all) e = go(few_u_kernel<XT, TY, RS, MT>, nub, tiles, a, st);
+  return e;
+}
+template <int XT, int TY, int RS>
+hipError_t route_rs(const FewArgs& a, hipStream_t st) {
+  return a.T <= 16 ? route_mt<XT, TY, RS, 1>(a, st) : route_mt<XT, TY, RS, 2>(a, st);
+}
+
+template <int XT, int TY, bool Q4>
+hipError_t up_q(const FewArgs& a, hipStream_t st) {
+  const unsigned grid = static_cast<unsigned>(a.G < a.T * a.kg ? a.G : a.T * a.kg) * (a.f * a.Pin / 32);
+  const size_t lds = static_cast<size_t>(NW) * 2 * 256 * sizeof(float);
+  return a.T <= 16 ? go(few_up_kernel<XT, TY, Q4, 1>, grid, lds, a, st)
+                   : go(few_up_kernel<XT, TY, Q4, 2>, grid, 2 * lds, a, st);
+}
+
+template <int XT, int TY, bool Q4>
+hipError_t down_q(const FewArgs& a, hipStream_t st) {
+  const unsigned grid = a.d / 16;
+  const int groups = a.G < a.T * a.kg ? a.G : a.T * a.kg;
+  const int nv = a.resid != RS_NONE ? a.T * a.k * 16 : 0;
+  const int mt = TY == DT_F32 ? (a.T <= 16 ? 1 : 2) : a.T <= 8 ? 1 : a.T <= 16 ? 2 : 4;
+  const size_t lds = sizeof(float) * (static_cast<size_t>(NW) * mt * 256 + nv + (nv > NT ? nv : NT)) +
+                     sizeof(int16_t) * groups * FEW_MAX_T;
+  if (mt == 1) return go(few_down_kernel<XT, TY, Q4, 1>, grid, lds, a, st);
+  if (mt == 2) return go(few_down_kernel<XT, TY, Q4, 2>, grid, lds, a, st);
+  if constexpr (TY != DT_F32) return go(few_down_kernel<XT, TY, Q4, 4>, grid, lds, a, st);
+  return hipErrorInvalidValue;
+}
+
+}  // namespace
+
+int few_router_splits(int d) {
+  // two 32-deep units per wavefront keep the matrix's loads in flight; at most
+  // 8 partial scores for the selection to add
+  const int s = d / 32 / (2 * NW);
+  return s < 1 ? 1 : s > 8 ? 8 : s;
+}
+
+hipError_t launch_few_route(int xt, int ty, const FewArgs& a, hipStream_t st) {
+  const int rs = a.resid == RS_NONE ? 0 : a.resid == RS_INT4 ? 2 : 1;
+  switch (xt * 16 + ty * 4 + rs) {
+    case 0: return route_rs<DT_F32, DT_F32, RS_NONE>(a, st);
+    case 1: return route_rs<DT_F32, DT_F32, RS_F32>(a, st);
+    case 16 + 4: return route_rs<DT_F16, DT_F16, RS_NONE>(a, st);
+    case 16 + 5: return route_rs<DT_F16, DT_F16, RS_F16>(a, st);
+    case 16 + 6: return route_rs<DT_F16, DT_F16, RS_INT4>(a, st);
+    case 32 + 8: return route_rs<DT_BF16, DT_BF16, RS_NONE>(a, st);
+    case 32 + 10: return route_rs<DT_BF16, DT_BF16, RS_INT4>(a, st);
+    case 32 + 4: return route_rs<DT_BF16, DT_F16, RS_NONE>(a, st);
+    case 32 + 5: return route_rs<DT_BF16, DT_F16, RS_F16>(a, st);
+    case 32 + 6: return route_rs<DT_BF16, DT_F16, RS_INT4>(a, st);
+  }
+  return hipErrorInvalidValue;
+}
+
+hipError_t launch_few_up(int xt, int ty, bool q4, const FewArgs& a, hipStream_t st) {
+  switch (xt * 8 + ty * 2 + (q4 ? 1 : 0)) {
+    case 0: return up_q<DT_F32, DT_F32, false>(a, st);
+    case 8 + 2: return up_q<DT_F16, DT_F16, false>(a, st);
+    case 8 + 3: return up_q<DT_F16, DT_F16, true>(a, st);
+    case 16 + 4: return up_q<DT_BF16, DT_BF16, false>(a, st);
+    case 16 + 5: return up_q<DT_BF16, DT_BF16, true>(a, st);
+    case 16 + 2: return up_q<DT_BF16, DT_F16, false>(a, st);
+  }
+  return hipErrorInvalidValue;
+}
+
+hipError_t launch_few_down(int xt, int ty, bool q4, const FewArgs& a, hipStream_t st) {
+  switch (xt * 8 + ty * 2 + (q4 ? 1 : 0)) {
+    case 0: return down_q<DT_F32, DT_F32, false>(a, st);
+    case 8 + 2: return down_q<DT_F16, DT_F16, false>(a, st);
+    case 8 + 3: return down_q<DT_F16, DT_F16, true>(a, st);
+    case 16 + 4: return down_q<DT_BF16, DT_BF16, false>(a, st);
+    case 16 + 5: return down_q<DT_BF16, DT_BF16, true>(a, st);
+    case 16 + 2: return down_q<DT_BF16, DT_F16, false>(a, st);
+  }
+  return hipErrorInvalidValue;
+}
+
+hipError_t launch_repack(int es, const void* src0, const void* src1, int groups, int n_in, int n_out, void* dst,
+                         hipStream_t st) {
+  const long per_group = static_cast<long>(n_in) * n_out * (src1 ? 2 : 1) / 8;
+  const dim3 grid(static_cast<unsigned>((per_group + 255) / 256), groups);
+  if (es == 4)
+    hipLaunchKernelGGL(repack_kernel<float>, grid, dim3(256), 0, st, static_cast<const float*>(src0),
+                       static_cast<const float*>(src1), n_in, n_out, static_cast<float*>(dst), per_group);
+  else
+    hipLaunchKernelGGL(repack_kernel<uint16_t>, grid, dim3(256), 0, st, static_cast<const uint16_t*>(src0),
+                       static_cast<const uint16_t*>(src1), n_in, n_out, static_cast<uint16_t*>(dst), per_group);
+  return hipGetLastError();
+}
+
+}  // namespace cefn

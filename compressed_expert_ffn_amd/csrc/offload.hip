@@ -95,6 +95,7 @@ int moe_offload_enable(moe_handle* h, int32_t slots) {
   if (!h) return fail(MOE_ERR_INVALID_ARG, "null handle");
   const moe_config& c = h->cfg;
   if (h->off) return fail(MOE_ERR_INVALID_ARG, "offload already enabled");
+  if (c.base_dtype == MOE_INT4_G32) return fail(MOE_ERR_UNSUPPORTED, "a 4-bit base cannot be offloaded");
   if (slots < 1 || slots > c.G) return fail(MOE_ERR_INVALID_ARG, "slots=%d outside [1, G=%d]", slots, c.G);
   if (hipDeviceSynchronize() != hipSuccess) return fail(MOE_ERR_HIP, "synchronise");
   delete_bwd(h);  // the backward layouts are not kept for an offloaded handle

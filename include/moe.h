@@ -54,7 +54,10 @@ enum moe_status {
   MOE_ERR_HIP = 4          /* a HIP runtime call failed */
 };
 
-typedef enum { MOE_F32 = 0, MOE_F16 = 1, MOE_BF16 = 2 } moe_dtype;
+/* MOE_INT4_G32 is a storage form of the base only: 4-bit codes with one fp16
+ * scale per 32 consecutive rows (d_in) of a column, by the rule of
+ * MOE_RESID_INT4_G32 below. */
+typedef enum { MOE_F32 = 0, MOE_F16 = 1, MOE_BF16 = 2, MOE_INT4_G32 = 3 } moe_dtype;
 
 /* Residual factor storage.  INT4_G32: symmetric 4-bit codes q in [-8, 7]
  * with one fp16 scale per 32 consecutive entries along the factor's first
@@ -77,8 +80,10 @@ typedef enum { MOE_ACT_GELU_TANH = 0, MOE_ACT_SWIGLU = 1 } moe_act;
  * top_groups*top_experts <= 16; d and f multiples of 64; r in {0} or 1..16
  * (r = 0 iff resid == MOE_RESID_NONE);
  * dtype mixes (x, base): (F32, F32), (F16, F16), (BF16, BF16), (BF16, F16)
- * -- bf16 activations are converted to fp16 for an fp16 base; residual F32
- * needs an F32 base, F16 an F16 base, INT4_G32 an F16 or BF16 base. */
+ * -- bf16 activations are converted to fp16 for an fp16 base -- and, for
+ * decoding a few tokens (moe_forward_few and moe_route only), (F16, INT4_G32)
+ * and (BF16, INT4_G32); residual F32 needs an F32 base, F16 an F16 base,
+ * INT4_G32 an F16, BF16 or INT4_G32 base. */
 typedef struct {
   int32_t T_max;       /* largest T a later call may pass */
   int32_t d;           /* model width (input and output of the layer) */
@@ -97,7 +102,8 @@ typedef struct {
 /* Weights, row-major, read only during moe_create (the caller keeps
  * ownership).  on_device = 0: every pointer is a HOST pointer; on_device = 1:
  * every pointer is a DEVICE pointer on the current HIP device (moe_create
- * reads them back before packing, so they may be freed once it returns).
+ * waits for its stream argument first, and they may be freed once it returns;
+ * the base is packed on the device, the rest read back).
  * Projections in order (gate, up, down) for SwiGLU, (w1, w2) for GELU;
  * d_in x d_out is d x f for the input projections and f x d for the output
  * projection.
@@ -105,7 +111,8 @@ typedef struct {
  *   W_exp       float32 [G][d][K]     (ignored, may be NULL, when K == 1)
  *   group_bias  float32 [G]           (NULL = zeros)
  *   expert_bias float32 [E]           (NULL = zeros; ignored when K == 1)
- *   base[p]     base_dtype [G][d_in][d_out]   (bf16 as raw uint16 bits)
+ *   base[p]     base_dtype [G][d_in][d_out]   (bf16 as raw uint16 bits;
+ *                               float32 for INT4_G32, quantised in moe_create)
  *   A[p]        [E][d_in][r]    float32 for RESID_F32 and RESID_INT4_G32
  *   B[p]        [E][d_out][r]   (INT4 is quantised inside moe_create from
  *                               these float32 values), float16 for F16;
@@ -193,6 +200,24 @@ int moe_forward(moe_handle* h, const void* X, int32_t T, void* Y,
 int moe_forward_noalloc(moe_handle* h, const void* X, int32_t T, void* Y,
                         const moe_route_out* routing, void* stream);
 
+/* The whole layer for a few tokens, 0 <= T <= min(T_max, 32): what
+ * moe_forward computes, by kernels that stream the weights of the touched
+ * groups once for all tokens, in three launches (four where the residual
+ * input factors are so many that only the chosen experts' are read).  The
+ * only forward pass of a layer with a 4-bit base.  X (on a 16-byte boundary)
+ * and Y as moe_forward, routing too; the handle's device must be current.
+ * Sums and everything between the kernels are held to FP32 accuracy and Y is
+ * rounded once, so results differ from moe_forward's by the roundings that
+ * one makes (hidden sums and rank products in 16 bits), and the choice of an
+ * expert may differ where two scores agree to FP32 rounding.  A token's
+ * result depends on X's other rows only through the order of its sums; equal
+ * calls give equal bits.  For a 4-bit base, activations and gate-weighted
+ * hidden sums that are infinite or NaN give NaN rather than an infinity.
+ * Enqueue only, and capturable, as moe_forward; one handle is not re-entrant
+ * (this entry has a workspace of its own in the handle). */
+int moe_forward_few(moe_handle* h, const void* X, int32_t T, void* Y, const moe_route_out* routing,
+                    void* stream);
+
 /* Gradients of the layer, caller-owned DEVICE buffers, float32, row-major,
  * in the shapes of moe_weights (written, not accumulated). */
 typedef struct {
@@ -235,8 +260,8 @@ int moe_backward(moe_handle* h, const void* X, int32_t T, const void* dY, void* 
  * use, prefetch from the current batch's routing what the next batch will
  * need).  moe_offload_enable converts a created handle (synchronous;
  * 1 <= slots <= G); afterwards only moe_forward_offload and moe_route run on
- * it (moe_forward, moe_forward_noalloc and moe_backward return
- * MOE_ERR_UNSUPPORTED). */
+ * it (moe_forward, moe_forward_noalloc, moe_forward_few and moe_backward
+ * return MOE_ERR_UNSUPPORTED).  Not for a 4-bit base. */
 typedef struct {
   int64_t calls;        /* moe_forward_offload calls */
   int64_t group_loads;  /* groups copied in because a batch needed them */
