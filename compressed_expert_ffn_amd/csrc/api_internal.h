@@ -42,12 +42,12 @@ struct Workspace {
 };
 
 // Workspace of moe_forward_few, for T_cap = min(T_max, 32) tokens.  The ticket
-// is zero between passes; the last row of H stays zero.
+// is zero between passes; the last rows of H and V stay zero.
 struct FewState {
   int T_cap = 0;
-  int *idx = nullptr, *gidx = nullptr, *glist = nullptr, *ticket = nullptr;
-  int16_t* grow = nullptr;
-  float *w = nullptr, *L = nullptr, *U = nullptr, *Vp = nullptr;
+  int *idx = nullptr, *gidx = nullptr, *glist = nullptr, *elist = nullptr, *ticket = nullptr;
+  int16_t *grow = nullptr, *eslot = nullptr;
+  float *w = nullptr, *L = nullptr, *U = nullptr, *Vp = nullptr, *V = nullptr;
   void* H = nullptr;
 };
 

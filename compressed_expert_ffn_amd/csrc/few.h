@@ -8,7 +8,7 @@
 namespace cefn {
 
 constexpr int FEW_MAX_T = 32;   // tokens a pass takes: two 16-row MFMA tiles
-constexpr int FEW_WAVES = 16;   // wavefronts per workgroup of every kernel
+constexpr int FEW_WAVES = 16;   // wavefronts per workgroup (8 in the input projection's large grids)
 
 struct FewArgs {
   const void* X;  // [T][d]
@@ -30,6 +30,10 @@ struct FewArgs {
   // grow[a][t] the row t*kg + rank of token t in it, or -1
   int* glist;
   int16_t* grow;  // [min(G, T*kg)][FEW_MAX_T]
+  // the same of the touched experts, for the residual tail: elist[0] of them,
+  // and eslot[i][t] the slot t*k + b of token t that chose expert elist[1 + i], or -1
+  int* elist;
+  int16_t* eslot;  // [min(E, T*k)][FEW_MAX_T]
   // residual input factors
   const void* At;
   const uint16_t* At_s;
@@ -47,6 +51,9 @@ struct FewArgs {
   int NV;
   const uint16_t *B1_s, *Ad_s, *Bd_s;
   float* Vp;      // [f blocks][T*k][16] partials of h A_down
+  float* V;       // [T*k + 1][16]: their sums (v_sum), and a row of zeros at zero_slot
+  int v_sum;      // 1: summed by a launch of its own; 0: by every workgroup of the down product
+  int zero_slot;
   void* H;        // [T*kg][planes][f]: gate-weighted hidden sums, fp32 (one plane), or two 16-bit planes, value and rest
   int zero_row;   // row of H that stays zero (the last of the workspace)
 };
@@ -54,7 +61,9 @@ struct FewArgs {
 // Columns of f per input-projection workgroup (32 weight columns).
 inline __host__ __device__ int few_fcols(int Pin) { return 32 / Pin; }
 // k splits of the score product over workgroups.
-int few_router_splits(int d);
+int few_router_splits(int d, int NCp);
+// Whether the partials of h A_down are summed by a launch of their own.
+bool few_v_sum(const FewArgs& a);
 hipError_t launch_few_route(int xt, int ty, const FewArgs& a, hipStream_t st);
 hipError_t launch_few_up(int xt, int ty, bool q4, const FewArgs& a, hipStream_t st);
 hipError_t launch_few_down(int xt, int ty, bool q4, const FewArgs& a, hipStream_t st);

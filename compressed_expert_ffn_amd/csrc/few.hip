@@ -106,7 +106,7 @@ __device__ __forceinline__ void factor8(int resid, const void* base, long i8, co
 }
 
 // ---------------------------------------------------------------- route --
-// Scores of 32 columns over this workgroup's part of the depth, in fp32
+// Scores of 16 columns over this workgroup's part of the depth, in fp32
 // MFMAs (the router runs in FP32; the matrix is small and the MFMAs hide
 // behind its loads).
 template <int XT, int MT>
@@ -120,55 +120,53 @@ __device__ void score_block(const FewArgs& a, int cb, int split, float* red) {
 #pragma unroll
   for (int m = 0; m < MT; ++m)
     xp[m] = static_cast<const XE*>(a.X) + static_cast<long>(min(16 * m + l, a.T - 1)) * a.d + 8 * q;
-  // column cb*32 + 16 c + l, depth 8 q .. of each 32
-  const float* wp = a.Wr + (static_cast<long>(q >> 1) * a.NCp + cb * 32 + l) * 16 + 8 * (q & 1);
+  // column cb*16 + l, depth 8 q .. of each 32
+  const float* wp = a.Wr + (static_cast<long>(q >> 1) * a.NCp + cb * 16 + l) * 16 + 8 * (q & 1);
   const long wstep = 2L * a.NCp * 16;
   struct Slot {
     Raw<XT> x[MT];
-    f8 w[2];
+    f8 w;
   };
-  f4v acc[2][MT];
+  f4v acc[MT];
 #pragma unroll
-  for (int c = 0; c < 2; ++c)
-#pragma unroll
-    for (int m = 0; m < MT; ++m) acc[c][m] = f4v{0.f, 0.f, 0.f, 0.f};
-  stream_units<2, Slot>(
+  for (int m = 0; m < MT; ++m) acc[m] = f4v{0.f, 0.f, 0.f, 0.f};
+  stream_units<3, Slot>(
       u1 - u0,
       [&](int i, Slot& s) {
         const long u = u0 + i;
+        s.w = load_frag<DT_F32>(wp + u * wstep);
 #pragma unroll
         for (int m = 0; m < MT; ++m) s.x[m] = load_raw<XT>(xp[m] + u * 32);
-#pragma unroll
-        for (int c = 0; c < 2; ++c) s.w[c] = load_frag<DT_F32>(wp + u * wstep + c * 256);
       },
       [&](const Slot& s) {
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const f8 x = raw_to_frag<XT, DT_F32>(s.x[m]);
-#pragma unroll
-          for (int c = 0; c < 2; ++c) acc[c][m] = mfma16<DT_F32>(x, s.w[c], acc[c][m]);
-        }
+        for (int m = 0; m < MT; ++m) acc[m] = mfma16<DT_F32>(raw_to_frag<XT, DT_F32>(s.x[m]), s.w, acc[m]);
       });
 #pragma unroll
-  for (int c = 0; c < 2; ++c)
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-      *reinterpret_cast<f4v*>(red + ((wave * 2 + c) * MT + m) * 256 + lane * 4) = acc[c][m];
+  for (int m = 0; m < MT; ++m) *reinterpret_cast<f4v*>(red + (wave * MT + m) * 256 + lane * 4) = acc[m];
 }
 
-// Sum over wavefronts of element (row, column) of a 32-column block left by
-// score_block or u_block.
-template <int MT>
+// Sum over NWV wavefronts of element (row, column) of a block of NS * 16
+// columns, each wavefront's part held as [NS][MT] MFMA accumulators.
+template <int NWV, int NS, int MT>
 __device__ __forceinline__ float block_sum(const float* red, int row, int col) {
   const int r = row & 15;
   const int at = ((col >> 4) * MT + (row >> 4)) * 256 + (16 * (r >> 2) + (col & 15)) * 4 + (r & 3);
   float s = 0.f;
 #pragma unroll
-  for (int w = 0; w < NW; ++w) s += red[w * 2 * MT * 256 + at];
+  for (int w = 0; w < NWV; ++w) s += red[w * NS * MT * 256 + at];
   return s;
 }
 
 // u = x A for the 32 factor columns of block nb of group g.
+//
+// 4-bit factors: a 64-deep unit of the block is 256 words, word 64 q' + 32 h +
+// c for depths 64 u + 32 h + 8 q' .. and column c.  Lane 16 q + l takes words
+// 4 (16 q + l) .. + 3 in one load: columns 4 (l % 8) + i at half h = l / 8,
+// so the 16 columns of an MFMA are 8 real ones at both halves of the depth.
+// Each word multiplies the activations of both halves and the lane keeps its
+// own; two MFMAs for one, but a fourth of the loads (4-byte loads of each
+// half's 16 columns took 6.4 us of a 256-expert layer's launch).
 template <int XT, int TY, bool INT4, int MT>
 __device__ void u_block(const FewArgs& a, int g, int nb, float* red) {
   using XE = typename Elem<XT>::T;
@@ -176,62 +174,95 @@ __device__ void u_block(const FewArgs& a, int g, int nb, float* red) {
   const int wave = wave_id(), lane = threadIdx.x & 63, l = lane & 15, q = lane >> 4;
   const int n64 = a.d / 64;
   const int u0 = n64 * wave / NW, u1 = n64 * (wave + 1) / NW;
+  const int cols = a.K * a.Pin * 16;  // column (j * Pin + p) * 16 + rho of the group
   const XE* xp[MT];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
     xp[m] = static_cast<const XE*>(a.X) + static_cast<long>(min(16 * m + l, a.T - 1)) * a.d + 8 * q;
-  // fragment 4 u + q of the block, lane half h, columns 16 c + l: depth 64 u + 32 h + 8 q ..
-  const long at = (static_cast<long>(nb) * (a.d / 16) + q) * 64 + l;
-  f4v acc[2][MT];
-#pragma unroll
-  for (int c = 0; c < 2; ++c)
-#pragma unroll
-    for (int m = 0; m < MT; ++m) acc[c][m] = f4v{0.f, 0.f, 0.f, 0.f};
   if constexpr (INT4) {
-    const uint32_t* wp = static_cast<const uint32_t*>(a.At) + g * a.at_gs + at;
-    const uint16_t* sp = a.At_s + g * a.at_sgs + static_cast<long>(nb) * (a.d / 32) * 32 + l;
+    const int h = l >> 3;
+    const uint32_t* wp =
+        static_cast<const uint32_t*>(a.At) + g * a.at_gs + static_cast<long>(nb) * (a.d / 16) * 64 + 4 * lane;
+    const uint16_t* sp =
+        a.At_s + g * a.at_sgs + (static_cast<long>(nb) * (a.d / 32) + h) * 32 + 4 * (l & 7);
+    f4v acc[4][MT];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int m = 0; m < MT; ++m) acc[i][m] = f4v{0.f, 0.f, 0.f, 0.f};
     struct Slot {
       Raw<XT> x[2][MT];
-      uint32_t w[2][2];
-      uint16_t s[2][2];
+      u4v w;
+      u2v s;
     };
-    stream_units<2, Slot>(
+    const B ones = q4_ones<TY>();
+    stream_units<MT == 1 ? 4 : 2, Slot>(
         u1 - u0,
         [&](int i, Slot& s) {
           const long u = u0 + i;
+          s.w = *reinterpret_cast<const u4v*>(wp + u * 256);
+          s.s = load_scales<4>(sp + u * 64);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
+          for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
-            for (int m = 0; m < MT; ++m) s.x[h][m] = load_raw<XT>(xp[m] + u * 64 + 32 * h);
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              s.w[h][c] = wp[u * 256 + 32 * h + 16 * c];
-              s.s[h][c] = sp[(2 * u + h) * 32 + 16 * c];
-            }
-          }
+            for (int m = 0; m < MT; ++m) s.x[hh][m] = load_raw<XT>(xp[m] + u * 64 + 32 * hh);
         },
         [&](const Slot& s) {
+          B x[2][MT];
+          f4v off[2][MT];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            B x[MT];
+          for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
-            for (int m = 0; m < MT; ++m) x[m] = raw_to_frag<XT, TY>(s.x[h][m]);
+            for (int m = 0; m < MT; ++m) {
+              x[hh][m] = raw_to_frag<XT, TY>(s.x[hh][m]);
+              const f4v sum = mfma16<TY>(x[hh][m], ones, f4v{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const B b = int4_frag_1scale<TY>(s.w[h][c], 0x3C00);  // the codes themselves
-              const float sc = f16_bits_to_f32(s.s[h][c]);
+              for (int r = 0; r < 4; ++r) off[hh][m][r] = -kQ4Offset * sum[r];
+            }
 #pragma unroll
-              for (int m = 0; m < MT; ++m) {
-                const f4v p = mfma16<TY>(x[m], b, f4v{0.f, 0.f, 0.f, 0.f});
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t word = s.w[i];
+            const B b = q4_frag_plain<TY>(word);
+            const float sc = scale_at(s.s, i);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[c][m][i] += sc * p[i];
-              }
+            for (int m = 0; m < MT; ++m) {
+              const f4v p0 = mfma16<TY>(x[0][m], b, off[0][m]);
+              const f4v p1 = mfma16<TY>(x[1][m], b, off[1][m]);
+#pragma unroll
+              for (int r = 0; r < 4; ++r) acc[i][m][r] += sc * (h ? p1[r] : p0[r]);
             }
           }
         });
+    // the two halves of a column sit 8 lanes apart
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        f4v v;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] = acc[i][m][r] + __shfl_xor(acc[i][m][r], 8);
+        if (h == 0) *reinterpret_cast<f4v*>(red + ((wave * 4 + i) * MT + m) * 128 + (8 * q + l) * 4) = v;
+      }
+    __syncthreads();
+    for (int v = threadIdx.x; v < a.T * 32; v += NT) {
+      const int row = v >> 5, col = v & 31, r = row & 15;
+      if (nb * 32 + col >= cols) continue;
+      const int at = ((col & 3) * MT + (row >> 4)) * 128 + (8 * (r >> 2) + (col >> 2)) * 4 + (r & 3);
+      float s = 0.f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) s += red[w * 4 * MT * 128 + at];
+      a.U[(static_cast<long>(row) * a.G + g) * cols + nb * 32 + col] = s * Q4Type<TY>::undo;
+    }
   } else {
     constexpr int es = TY == DT_F32 ? 4 : 2;
-    const char* wp = static_cast<const char*>(a.At) + (g * a.at_gs + at * 8) * es;
+    // fragment 4 u + q of the block, lane half h, columns 16 c + l: depth 64 u + 32 h + 8 q ..
+    const char* wp =
+        static_cast<const char*>(a.At) + (g * a.at_gs + ((static_cast<long>(nb) * (a.d / 16) + q) * 64 + l) * 8) * es;
+    f4v acc[2][MT];
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int m = 0; m < MT; ++m) acc[c][m] = f4v{0.f, 0.f, 0.f, 0.f};
     struct Slot {
       Raw<XT> x[2][MT];
       B w[2][2];
@@ -258,152 +289,191 @@ __device__ void u_block(const FewArgs& a, int g, int nb, float* red) {
               for (int c = 0; c < 2; ++c) acc[c][m] = mfma16<TY>(x, s.w[h][c], acc[c][m]);
             }
         });
-  }
 #pragma unroll
-  for (int c = 0; c < 2; ++c)
+    for (int c = 0; c < 2; ++c)
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-      *reinterpret_cast<f4v*>(red + ((wave * 2 + c) * MT + m) * 256 + lane * 4) = acc[c][m];
-  __syncthreads();
-  // column (j * Pin + p) * 16 + rho of the group
-  const int cols = a.K * a.Pin * 16;
-  for (int v = threadIdx.x; v < a.T * 32; v += NT) {
-    const int row = v >> 5, col = v & 31;
-    if (nb * 32 + col >= cols) continue;
-    a.U[(static_cast<long>(row) * a.G + g) * cols + nb * 32 + col] = block_sum<MT>(red, row, col);
+      for (int m = 0; m < MT; ++m)
+        *reinterpret_cast<f4v*>(red + ((wave * 2 + c) * MT + m) * 256 + lane * 4) = acc[c][m];
+    __syncthreads();
+    for (int v = threadIdx.x; v < a.T * 32; v += NT) {
+      const int row = v >> 5, col = v & 31;
+      if (nb * 32 + col >= cols) continue;
+      a.U[(static_cast<long>(row) * a.G + g) * cols + nb * 32 + col] = block_sum<NW, 2, MT>(red, row, col);
+    }
   }
 }
 
-// Selection for every token, the touched groups, and the caller's lists, by
-// one workgroup.  sc: [16][NC] scores of 16 tokens at a time.
-__device__ void select_all(const FewArgs& a, float* sc, int* sidx, int* sgid, int* cnt) {
+// LDS of the selecting workgroup.
+struct SelectLds {
+  int idx[FEW_MAX_T * MAX_SLOTS], gid[FEW_MAX_T * MAX_KG];
+  float pg[FEW_MAX_T * MAX_KG];
+  int gcount[256], ecount[1024], gpos[256], epos[1024];
+  int wsum[NW];
+  int last;
+};
+
+// Position of each non-zero count among the non-zero ones (id order), by all
+// threads for up to NT counts; returns their number.
+__device__ int compact(const int* count, int n, int* pos, int* wsum) {
   const int tid = threadIdx.x, wave = wave_id(), lane = tid & 63;
-  const int NC = a.G + (a.K > 1 ? a.G * a.K : 0);
-  for (int t0 = 0; t0 < a.T; t0 += NW) {
-    const int nt = min(NW, a.T - t0);
-    for (int e = tid; e < nt * NC; e += NT) {
-      const int tk = e / NC, c = e - tk * NC;
-      const float* p = a.L + static_cast<long>(t0 + tk) * a.NCp + c;
-      const long stride = static_cast<long>(a.T) * a.NCp;
-      float part[8];
+  const bool on = tid < n && count[tid] > 0;
+  const unsigned long long m = __ballot(on);
+  if (lane == 0) wsum[wave] = __popcll(m);
+  __syncthreads();
+  int before = 0, total = 0;
 #pragma unroll
-      for (int s = 0; s < 8; ++s)
-        part[s] = s < a.nsplit ? __hip_atomic_load(p + s * stride, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0.f;
-      float v = ((part[0] + part[1]) + (part[2] + part[3])) + ((part[4] + part[5]) + (part[6] + part[7]));
-      if (c < a.G) {
-        if (a.gbias) v += a.gbias[c];
-      } else if (a.ebias) {
-        v += a.ebias[c - a.G];
-      }
-      sc[e] = v;
-    }
-    __syncthreads();
-    if (wave < nt) {
-      // gates: softmax over the chosen groups times softmax over the chosen
-      // experts of each
-      const int t = t0 + wave;
-      const float* st = sc + wave * NC;
-      float gvl, evl;
-      int gil, eil;
-      wave_topk(st, a.G, a.kg, lane, gvl, gil);
-      const float g0 = __shfl(gvl, 0);
-      float ps = 0.f;
-      for (int i = 0; i < a.kg; ++i) ps += expf(__shfl(gvl, i) - g0);
-      for (int ga = 0; ga < a.kg; ++ga) {
-        const int g = __shfl(gil, ga);
-        const float pg = expf(__shfl(gvl, ga) - g0) / ps;
-        if (a.K == 1) {
-          if (lane == 0) {
-            sidx[t * a.k + ga] = g;
-            a.idx[t * a.k + ga] = g;
-            a.w[t * a.k + ga] = pg;
-          }
-        } else {
-          wave_topk(st + a.G + g * a.K, a.K, a.ke, lane, evl, eil);
-          const float e0 = __shfl(evl, 0);
-          float qs = 0.f;
-          for (int b = 0; b < a.ke; ++b) qs += expf(__shfl(evl, b) - e0);
-          if (lane < a.ke) {
-            const int slot = t * a.k + ga * a.ke + lane;
-            sidx[slot] = g * a.K + eil;
-            a.idx[slot] = g * a.K + eil;
-            a.w[slot] = pg * (expf(evl - e0) / qs);
-          }
-        }
-        if (lane == 0) {
-          sgid[t * a.kg + ga] = g;
-          a.gidx[t * a.kg + ga] = g;
-        }
-      }
-    }
-    __syncthreads();
+  for (int w = 0; w < NW; ++w) {
+    const int c = wsum[w];
+    before += w < wave ? c : 0;
+    total += c;
   }
-  // tokens per group, then the touched groups in ascending order
-  const int ng = a.T * a.kg, na = a.T * a.k;
-  if (tid < a.G) {
-    int n = 0;
-    for (int i = 0; i < ng; ++i) n += sgid[i] == tid ? 1 : 0;
-    cnt[tid] = n;
+  if (on) pos[tid] = before + __popcll(m & ((1ull << lane) - 1));
+  __syncthreads();
+  return total;
+}
+
+// Scores of tokens t0 .. t0 + nt - 1 into sc [nt][NC], biases included: the
+// parts other workgroups stored, several elements' loads in flight at once.
+__device__ void gather_scores(const FewArgs& a, int t0, int nt, int NC, float* sc) {
+  const long stride = static_cast<long>(a.T) * a.NCp;
+  const int total = nt * NC;
+  for (int e0 = threadIdx.x; e0 < total; e0 += 4 * NT) {
+    float part[4][4], bias[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int e = e0 + j * NT;
+      const bool ok = e < total;
+      const int tk = ok ? e / NC : 0, c = ok ? e - tk * NC : 0;
+      const float* p = a.L + static_cast<long>(t0 + tk) * a.NCp + c;
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        part[j][s] = ok && s < a.nsplit
+                         ? __hip_atomic_load(p + s * stride, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)
+                         : 0.f;
+      const float* bp = c < a.G ? a.gbias + c : a.ebias + (c - a.G);
+      bias[j] = ok && (c < a.G ? a.gbias != nullptr : a.ebias != nullptr) ? *bp : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (e0 + j * NT < total) sc[e0 + j * NT] = ((part[j][0] + part[j][1]) + (part[j][2] + part[j][3])) + bias[j];
+  }
+}
+
+// Selection for tokens t0 .. t0 + nt - 1 by one workgroup: larger score first,
+// ties to the lower index; gates are the softmax over the chosen groups times
+// the softmax over the chosen experts of each.
+__device__ void select_tokens(const FewArgs& a, int t0, int nt, int NC, const float* sc, SelectLds& s) {
+  const int wave = wave_id(), lane = threadIdx.x & 63;
+  for (int i = wave; i < nt; i += NW) {
+    const int t = t0 + i;
+    float v;
+    int g;
+    wave_topk(sc + i * NC, a.G, a.kg, lane, v, g);
+    const float e = lane < a.kg ? expf(v - __shfl(v, 0)) : 0.f;
+    float sum = 0.f;
+    for (int r = 0; r < a.kg; ++r) sum += __shfl(e, r);
+    if (lane < a.kg) {
+      s.gid[t * a.kg + lane] = g;
+      s.pg[t * a.kg + lane] = e / sum;
+      a.gidx[t * a.kg + lane] = g;
+      if (a.K == 1) {
+        s.idx[t * a.k + lane] = g;
+        a.idx[t * a.k + lane] = g;
+        a.w[t * a.k + lane] = e / sum;
+      }
+    }
   }
   __syncthreads();
-  if (tid < a.G) {
-    int at = 0, before = 0;
-    for (int g = 0; g < tid; ++g) {
-      at += cnt[g] > 0 ? 1 : 0;
-      before += cnt[g];
-    }
-    if (cnt[tid] > 0) {
-      a.glist[1 + at] = tid;
-      for (int t = 0; t < a.T; ++t) {
-        int row = -1;
-        for (int r = 0; r < a.kg; ++r)
-          if (sgid[t * a.kg + r] == tid) row = t * a.kg + r;
-        a.grow[at * FEW_MAX_T + t] = static_cast<int16_t>(row);
-      }
-    }
-    if (tid == a.G - 1) a.glist[0] = at + (cnt[tid] > 0 ? 1 : 0);
-    if (a.gcounts) a.gcounts[tid] = cnt[tid];
-    if (a.goffsets) {
-      a.goffsets[tid] = before;
-      if (tid == a.G - 1) a.goffsets[a.G] = ng;
+  if (a.K == 1) return;
+  for (int i = wave; i < nt * a.kg; i += NW) {
+    const int tr = t0 * a.kg + i, g = s.gid[tr];
+    float v;
+    int j;
+    wave_topk(sc + (i / a.kg) * NC + a.G + g * a.K, a.K, a.ke, lane, v, j);
+    const float e = lane < a.ke ? expf(v - __shfl(v, 0)) : 0.f;
+    float sum = 0.f;
+    for (int r = 0; r < a.ke; ++r) sum += __shfl(e, r);
+    if (lane < a.ke) {
+      const int slot = tr * a.ke + lane;  // (t * kg + rank) * ke + b
+      s.idx[slot] = g * a.K + j;
+      a.idx[slot] = g * a.K + j;
+      a.w[slot] = s.pg[tr] * (e / sum);
     }
   }
-  // an entry's place in its bin's list: the entries of lower bins, and those
-  // before it in its own (tokens ascend within a bin)
+  __syncthreads();
+}
+
+// The touched groups and experts with their tokens, and the caller's lists.
+// tab: room for (G + min(E, T*k)) * FEW_MAX_T int16.
+__device__ void make_lists(const FewArgs& a, SelectLds& s, int16_t* tab) {
+  const int tid = threadIdx.x;
+  const int ng = a.T * a.kg, na = a.T * a.k;
+  if (tid < a.G) s.gcount[tid] = 0;
+  if (tid < a.E) s.ecount[tid] = 0;
+  __syncthreads();
+  if (tid < ng) atomicAdd(&s.gcount[s.gid[tid]], 1);
+  if (tid < na) atomicAdd(&s.ecount[s.idx[tid]], 1);
+  __syncthreads();
+  const int tg = compact(s.gcount, a.G, s.gpos, s.wsum);
+  const int te = a.resid != RS_NONE ? compact(s.ecount, a.E, s.epos, s.wsum) : 0;
+  int16_t* etab = tab + a.G * FEW_MAX_T;
+  for (int i = tid; i < tg * (FEW_MAX_T / 2); i += NT) reinterpret_cast<int*>(tab)[i] = -1;
+  for (int i = tid; i < te * (FEW_MAX_T / 2); i += NT) reinterpret_cast<int*>(etab)[i] = -1;
+  __syncthreads();
+  if (tid < ng) tab[s.gpos[s.gid[tid]] * FEW_MAX_T + tid / a.kg] = static_cast<int16_t>(tid);
+  if (te && tid < na) etab[s.epos[s.idx[tid]] * FEW_MAX_T + tid / a.k] = static_cast<int16_t>(tid);
+  if (tid == 0) a.glist[0] = tg;
+  if (tid < a.G && s.gcount[tid] > 0) a.glist[1 + s.gpos[tid]] = tid;
+  if (te) {
+    if (tid == 0) a.elist[0] = te;
+    if (tid < a.E && s.ecount[tid] > 0) a.elist[1 + s.epos[tid]] = tid;
+  }
+  __syncthreads();
+  for (int i = tid; i < tg * (FEW_MAX_T / 2); i += NT)
+    reinterpret_cast<int*>(a.grow)[i] = reinterpret_cast<const int*>(tab)[i];
+  for (int i = tid; i < te * (FEW_MAX_T / 2); i += NT)
+    reinterpret_cast<int*>(a.eslot)[i] = reinterpret_cast<const int*>(etab)[i];
+  // the caller's lists: an entry's place in its bin's list is the entries of
+  // lower bins and those before it in its own (tokens ascend within a bin)
+  if (a.gcounts && tid < a.G) a.gcounts[tid] = s.gcount[tid];
+  if (a.counts && tid < a.E) a.counts[tid] = s.ecount[tid];
+  if (a.goffsets && tid <= a.G) {
+    int n = 0;
+    for (int i = 0; i < ng; ++i) n += s.gid[i] < tid ? 1 : 0;
+    a.goffsets[tid] = n;
+  }
+  if (a.offsets)
+    for (int e = tid; e <= a.E; e += NT) {
+      int n = 0;
+      for (int i = 0; i < na; ++i) n += s.idx[i] < e ? 1 : 0;
+      a.offsets[e] = n;
+    }
   if (a.gperm && tid < ng) {
     int at = 0;
-    for (int i = 0; i < ng; ++i) at += (sgid[i] < sgid[tid] || (sgid[i] == sgid[tid] && i < tid)) ? 1 : 0;
+    for (int i = 0; i < ng; ++i) at += (s.gid[i] < s.gid[tid] || (s.gid[i] == s.gid[tid] && i < tid)) ? 1 : 0;
     a.gperm[at] = tid / a.kg;
   }
   if (a.perm && tid < na) {
     int at = 0;
-    for (int i = 0; i < na; ++i) at += (sidx[i] < sidx[tid] || (sidx[i] == sidx[tid] && i < tid)) ? 1 : 0;
+    for (int i = 0; i < na; ++i) at += (s.idx[i] < s.idx[tid] || (s.idx[i] == s.idx[tid] && i < tid)) ? 1 : 0;
     a.perm[at] = tid / a.k;
-  }
-  if (a.counts || a.offsets) {
-    for (int e = tid; e < a.E; e += NT) {
-      int n = 0, before = 0;
-      for (int i = 0; i < na; ++i) {
-        n += sidx[i] == e ? 1 : 0;
-        before += sidx[i] < e ? 1 : 0;
-      }
-      if (a.counts) a.counts[e] = n;
-      if (a.offsets) {
-        a.offsets[e] = before;
-        if (e == a.E - 1) a.offsets[a.E] = na;
-      }
-    }
   }
 }
 
-// grid: the score blocks (32 columns x nsplit depth parts) first, then with
+// Tokens whose scores the selection holds in LDS at a time.
+__host__ __device__ inline int select_chunk(int T, int NC) {
+  const int n = 64 * 1024 / (4 * NC);
+  return n < T ? n : T;
+}
+
+// grid: the score blocks (16 columns x nsplit depth parts) first, then with
 // u_all one workgroup per 32 factor columns of every group.
 template <int XT, int TY, int RS, int MT>
 __global__ __launch_bounds__(NT) void few_route_kernel(FewArgs a) {
-  extern __shared__ __attribute__((aligned(16))) float red[];
-  __shared__ int sidx[FEW_MAX_T * MAX_SLOTS], sgid[FEW_MAX_T * MAX_KG], cnt[256];
-  __shared__ int last;
-  const int ncb = a.NCp / 32, nsb = ncb * a.nsplit;
+  extern __shared__ __attribute__((aligned(16))) float red[];  // partial tiles, then scores; last the lists' tables
+  __shared__ SelectLds s;
+  const int NC = a.G + (a.K > 1 ? a.G * a.K : 0);
+  const int ncb = (NC + 15) / 16, nsb = ncb * a.nsplit;
   if (static_cast<int>(blockIdx.x) >= nsb) {
     if constexpr (RS != RS_NONE) {
       const int ub = blockIdx.x - nsb, nbu = (a.K * a.Pin * 16 + 31) / 32;
@@ -411,26 +481,52 @@ __global__ __launch_bounds__(NT) void few_route_kernel(FewArgs a) {
     }
     return;
   }
+  float* sc = red + NW * MT * 256;
   const int cb = blockIdx.x % ncb, split = blockIdx.x / ncb;
   score_block<XT, MT>(a, cb, split, red);
   __syncthreads();
-  for (int v = threadIdx.x; v < a.T * 32; v += NT) {
-    const int row = v >> 5, col = v & 31;
-    __hip_atomic_store(a.L + (static_cast<long>(split) * a.T + row) * a.NCp + cb * 32 + col,
-                       block_sum<MT>(red, row, col), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if (nsb == 1) {
+    // up to 16 columns in all: this workgroup holds every score
+    for (int v = threadIdx.x; v < a.T * 16; v += NT) {
+      const int row = v >> 4, col = v & 15;
+      if (col >= NC) continue;
+      const float* bp = col < a.G ? a.gbias : a.ebias;
+      const float bias = bp ? bp[col < a.G ? col : col - a.G] : 0.f;
+      sc[row * NC + col] = block_sum<NW, 1, MT>(red, row, col) + bias;
+    }
+    __syncthreads();
+    select_tokens(a, 0, a.T, NC, sc, s);
+  } else {
+    // Scores go to memory past the caches (agent scope), each wavefront waits
+    // for its own stores, and the workgroup that counts itself in last selects;
+    // nobody waits for another.  The scores are read back past the caches too,
+    // so no cache needs writing back or dropping: a release fence here, which
+    // writes back the whole second-level cache, took 13 us of a 256-expert
+    // layer's launch.
+    for (int v = threadIdx.x; v < a.T * 16; v += NT) {
+      const int row = v >> 4, col = v & 15;
+      __hip_atomic_store(a.L + (static_cast<long>(split) * a.T + row) * a.NCp + cb * 16 + col,
+                         block_sum<NW, 1, MT>(red, row, col), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      const int n = __hip_atomic_fetch_add(a.ticket, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      s.last = n == nsb - 1 ? 1 : 0;
+      if (s.last) __hip_atomic_store(a.ticket, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);  // for the next pass
+    }
+    __syncthreads();
+    if (!s.last) return;
+    asm volatile("" ::: "memory");
+    const int chunk = select_chunk(a.T, NC);
+    for (int t0 = 0; t0 < a.T; t0 += chunk) {
+      const int nt = min(chunk, a.T - t0);
+      gather_scores(a, t0, nt, NC, sc);
+      __syncthreads();
+      select_tokens(a, t0, nt, NC, sc, s);
+    }
   }
-  // the last workgroup to have stored its scores selects; nobody waits
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    const int n = __hip_atomic_fetch_add(a.ticket, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
-    last = n == nsb - 1 ? 1 : 0;
-    if (last) __hip_atomic_store(a.ticket, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);  // for the next pass
-  }
-  __syncthreads();
-  if (!last) return;
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
-  select_all(a, red, sidx, sgid, cnt);
+  make_lists(a, s, reinterpret_cast<int16_t*>(red));
 }
 
 // U of the chosen experts only: one workgroup per 32 factor columns, idle
@@ -457,8 +553,8 @@ __global__ __launch_bounds__(NT) void few_u_kernel(FewArgs a) {
 // grid: (touched group a) x (blocks of FT = 32 / Pin columns of f).  A
 // workgroup's 32 weight columns are 16 of the gate and the same 16 of the up
 // projection (SwiGLU), or 32 of the one input projection (GELU).
-template <int XT, int TY, bool Q4, int MT>
-__global__ __launch_bounds__(NT) void few_up_kernel(FewArgs a) {
+template <int XT, int TY, bool Q4, int MT, int NWV>
+__global__ __launch_bounds__(NWV * 64) void few_up_kernel(FewArgs a) {
   using XE = typename Elem<XT>::T;
   using B = typename Frag<TY>::T;
   extern __shared__ __attribute__((aligned(16))) float red[];  // partial tiles, then hw [rows][ke][FT]
@@ -477,7 +573,7 @@ __global__ __launch_bounds__(NT) void few_up_kernel(FewArgs a) {
     if (lane == 0) nrows = __popcll(m);
   }
   const int n64 = a.d / 64;
-  const int u0 = n64 * wave / NW, u1 = n64 * (wave + 1) / NW;
+  const int u0 = n64 * wave / NWV, u1 = n64 * (wave + 1) / NWV;
   const XE* xp[MT];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
@@ -582,14 +678,14 @@ __global__ __launch_bounds__(NT) void few_up_kernel(FewArgs a) {
     for (int m = 0; m < MT; ++m)
       *reinterpret_cast<f4v*>(red + ((wave * 2 + c) * MT + m) * 256 + lane * 4) = acc[c][m];
   __syncthreads();
-  for (int v = threadIdx.x; v < MT * 16 * 32; v += NT) {
+  for (int v = threadIdx.x; v < MT * 16 * 32; v += NWV * 64) {
     const int row = v >> 5, col = v & 31;
-    z[col >> 4][row][col & 15] = block_sum<MT>(red, row, col);
+    z[col >> 4][row][col & 15] = block_sum<NWV, 2, MT>(red, row, col);
   }
   __syncthreads();  // partial tiles are read: red becomes hw
   float* hw = red;
   const int f0 = fb * FT, n = nrows;
-  for (int v = threadIdx.x; v < n * a.ke * FT; v += NT) {
+  for (int v = threadIdx.x; v < n * a.ke * FT; v += NWV * 64) {
     const int c = v % FT, b = (v / FT) % a.ke, i = v / (FT * a.ke);
     const int t = srow[i] >> 16, row = srow[i] & 0xFFFF;
     const int slot = t * a.k + (row - t * a.kg) * a.ke + b;
@@ -619,7 +715,7 @@ __global__ __launch_bounds__(NT) void few_up_kernel(FewArgs a) {
   }
   __syncthreads();
   constexpr int planes = TY == DT_F32 ? 1 : 2;
-  for (int v = threadIdx.x; v < n * FT; v += NT) {
+  for (int v = threadIdx.x; v < n * FT; v += NWV * 64) {
     const int c = v % FT, i = v / FT;
     const int row = srow[i] & 0xFFFF;
     float s = 0.f;
@@ -637,7 +733,7 @@ __global__ __launch_bounds__(NT) void few_up_kernel(FewArgs a) {
   }
   if (a.resid != RS_NONE) {
     const int f32 = f0 >> 5, st0 = (f0 >> 4) & 1;
-    for (int v = threadIdx.x; v < n * a.ke * 16; v += NT) {
+    for (int v = threadIdx.x; v < n * a.ke * 16; v += NWV * 64) {
       const int rho = v & 15, ib = v >> 4, i = ib / a.ke, b = ib - i * a.ke;
       const int t = srow[i] >> 16, row = srow[i] & 0xFFFF;
       const int slot = t * a.k + (row - t * a.kg) * a.ke + b;
@@ -660,6 +756,28 @@ __global__ __launch_bounds__(NT) void few_up_kernel(FewArgs a) {
   }
 }
 
+// ---------------------------------------------------------------- v sum --
+// V = the partials of h A_down summed over the blocks of f: 64 sums per
+// workgroup, their partials dealt to 16 wavefronts.
+__global__ __launch_bounds__(NT) void few_vsum_kernel(FewArgs a) {
+  __shared__ float part[NW][64];
+  const int nv = a.T * a.k * 16, nfb = a.f * a.Pin / 32;
+  const int wave = wave_id(), lane = threadIdx.x & 63, o = blockIdx.x * 64 + lane;
+  float s = 0.f;
+  if (o < nv) {
+#pragma unroll 8
+    for (int b = wave; b < nfb; b += NW) s += a.Vp[static_cast<long>(b) * nv + o];
+  }
+  part[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && o < nv) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) v += part[w][lane];
+    a.V[o] = v;
+  }
+}
+
 // ----------------------------------------------------------------- down --
 // grid: one workgroup per 16 columns of y.  Its wavefronts take consecutive
 // ranges of the touched groups' depths, laid end to end.  MFMA rows: with
@@ -667,45 +785,31 @@ __global__ __launch_bounds__(NT) void few_up_kernel(FewArgs a) {
 // the hidden sums are rows of their own: up to 8 tokens share one tile
 // (parts in rows 0-7 and 8-15), else tile m holds part m / (MT / 2) of
 // tokens 16 (m % (MT / 2)) + r.
+//
+// The residual tail V B_down is more depth of the same product: two touched
+// experts' 16 rank columns are one 32-deep step, whose rows are the V of the
+// tokens that chose the expert (zero for the others).  A 4-bit factor's scale
+// varies along the rank columns, i.e. along the depth, so it multiplies V,
+// which then splits into two 16-bit parts like the hidden sums.
+constexpr int kDownPartials = 16;  // partials of V a thread holds in registers
+
 template <int XT, int TY, bool Q4, int MT>
 __global__ __launch_bounds__(NT) void few_down_kernel(FewArgs a) {
   using B = typename Frag<TY>::T;
-  extern __shared__ __attribute__((aligned(16))) float red[];  // [NW][MT][256], then V, tail, grow
+  extern __shared__ __attribute__((aligned(16))) float red[];  // [NW][MT][256], then V and a zero row, partials, grow
   const int n = blockIdx.x, nv = a.resid != RS_NONE ? a.T * a.k * 16 : 0;
   float* V = red + NW * MT * 256;
-  float* tail = V + nv;
-  int16_t* grow = reinterpret_cast<int16_t*>(tail + max(nv, NT));
+  float* vpart = V + nv + 16;
+  int16_t* grow = reinterpret_cast<int16_t*>(vpart + (nv && !a.v_sum ? NT : 0));
   const int ng = a.glist[0];
   const int tid = threadIdx.x, wave = wave_id(), lane = tid & 63, l = lane & 15, q = lane >> 4;
-  for (int i = tid; i < ng * FEW_MAX_T; i += NT) grow[i] = a.grow[i];
-  if (nv) {
-    // V: the partials summed over the blocks of f, in an order set by T, k and f alone
-    const int nfb = a.f * a.Pin / 32;
-    if (nv <= NT) {
-      const int parts = NT / nv, p = tid / nv, o = tid - p * nv;
-      float s = 0.f;
-      if (p < parts)
-        for (int b = p; b < nfb; b += parts) s += a.Vp[static_cast<long>(b) * nv + o];
-      if (p < parts) tail[tid] = s;
-      __syncthreads();
-      if (tid < nv) {
-        float v = 0.f;
-        for (int i = 0; i < parts; ++i) v += tail[i * nv + tid];
-        V[tid] = v;
-      }
-    } else {
-      for (int o = tid; o < nv; o += NT) {
-        float s = 0.f;
-#pragma unroll 8
-        for (int b = 0; b < nfb; ++b) s += a.Vp[static_cast<long>(b) * nv + o];
-        V[o] = s;
-      }
-    }
-  }
+  for (int i = tid; i < ng * (FEW_MAX_T / 2); i += NT)
+    reinterpret_cast<int*>(grow)[i] = reinterpret_cast<const int*>(a.grow)[i];
   __syncthreads();
   constexpr int planes = TY == DT_F32 ? 1 : 2;
   constexpr int UNIT = Q4 ? 128 : 64, NS = UNIT / 32;
   constexpr bool packed = planes == 2 && MT == 1;
+  constexpr int TM = planes == 1 ? MT : MT > 1 ? MT / 2 : 1;  // tiles of tokens
   const int nf = (a.f + UNIT - 1) / UNIT;
   const int units = ng * nf;
   const int u0 = static_cast<int>(static_cast<long>(units) * wave / NW);
@@ -724,8 +828,7 @@ __global__ __launch_bounds__(NT) void few_down_kernel(FewArgs a) {
     const int g = a.glist[1 + ga];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      const int t = packed ? (l & 7) : planes == 1 ? 16 * m + l : 16 * (m % (MT > 1 ? MT / 2 : 1)) + l;
-      const int plane = packed ? l >> 3 : planes == 1 ? 0 : m / (MT > 1 ? MT / 2 : 1);
+      const int t = packed ? (l & 7) : 16 * (m % TM) + l, plane = packed ? l >> 3 : m / TM;
       const int row = t < a.T ? grow[ga * FEW_MAX_T + t] : -1;
       // a token that did not choose the group reads the row of zeros
       hp[m] = static_cast<const HE*>(a.H) + (static_cast<long>(row < 0 ? a.zero_row : row) * planes + plane) * a.f;
@@ -747,6 +850,103 @@ __global__ __launch_bounds__(NT) void few_down_kernel(FewArgs a) {
       kb = 0;
       ++ga;
       enter();
+    }
+  };
+  // the residual tail: steps of two touched experts, dealt to the wavefronts
+  const int te = nv ? a.elist[0] : 0, steps = (te + 1) / 2;
+  struct Tail {
+    u4v w[TY == DT_F32 ? 2 : 1], s;
+    int slot[TM];
+  } tail;
+  auto tail_load = [&](int i) {
+    const int ei = min(2 * i + (q >> 1), te - 1), hh = q & 1;
+    const int e = a.elist[1 + ei], g = e / a.K, j = e - g * a.K, n32 = n >> 1;
+    // rank column 8 hh .. of expert j in the permuted depth order
+    const int ks = 4 * (j >> 2) + 2 * (j & 1) + hh;
+    const long at = (static_cast<long>(n32) * (a.NV / 16) + ks) * 64 + 16 * (n & 1) + l + 32 * ((j >> 1) & 1);
+    if (a.resid == RS_INT4) {
+      tail.w[0][0] = static_cast<const uint32_t*>(a.Bd)[g * a.bd_gs + at];
+      tail.s = *reinterpret_cast<const u4v*>(a.Bd_s + (static_cast<long>(e) * (a.d / 32) + n32) * RPAD + 8 * hh);
+    } else {
+      const u4v* p = reinterpret_cast<const u4v*>(static_cast<const char*>(a.Bd) + (g * a.bd_gs + at * 8) * es);
+      tail.w[0] = p[0];
+      if constexpr (TY == DT_F32) tail.w[1] = p[1];
+    }
+#pragma unroll
+    for (int m = 0; m < TM; ++m) {
+      const int t = packed ? (l & 7) : 16 * m + l;
+      const int slot = t < a.T && 2 * i + (q >> 1) < te ? a.eslot[ei * FEW_MAX_T + t] : -1;
+      tail.slot[m] = slot < 0 ? a.T * a.k : slot;  // the row of zeros
+    }
+  };
+  auto tail_use = [&]() {
+    B b;
+    if constexpr (TY == DT_F32) {
+      Raw<DT_F32> r;
+      r.v[0] = tail.w[0];
+      r.v[1] = tail.w[1];
+      b = raw_to_frag<DT_F32, DT_F32>(r);
+    } else if (a.resid == RS_INT4) {
+      const uint32_t word = tail.w[0][0];
+      b = int4_frag_1scale<TY>(word, 0x3C00);  // the codes themselves
+    } else {
+      b = __builtin_bit_cast(B, tail.w[0]);
+    }
+#pragma unroll
+    for (int m = 0; m < TM; ++m) {
+      const float* vp = V + tail.slot[m] * 16 + 8 * (q & 1);
+      float v[8], rest[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        v[r] = vp[r];
+        if (TY != DT_F32 && a.resid == RS_INT4) {
+          const uint32_t w = tail.s[r >> 1];
+          v[r] *= f16_bits_to_f32(static_cast<uint16_t>((w >> (16 * (r & 1))) & 0xFFFFu));
+        }
+      }
+      const B hi = to_frag<TY>(v);
+      if constexpr (planes == 1) {
+        acc[m] = mfma16<TY>(hi, b, acc[m]);
+      } else {
+#pragma unroll
+        for (int r = 0; r < 8; ++r) rest[r] = v[r] - static_cast<float>(hi[r]);
+        const B lo = to_frag<TY>(rest);
+        if constexpr (packed) {
+          const u4v x = __builtin_bit_cast(u4v, hi), y = __builtin_bit_cast(u4v, lo);
+          acc[0] = mfma16<TY>(__builtin_bit_cast(B, l < 8 ? x : y), b, acc[0]);
+        } else {
+          acc[m] = mfma16<TY>(hi, b, acc[m]);
+          acc[TM + m] = mfma16<TY>(lo, b, acc[TM + m]);
+        }
+      }
+    }
+  };
+  // once the weights are under way: V into LDS (from the sum's launch, or
+  // summed here in an order set by T, k and f alone), the first tail step's loads
+  auto between = [&]() {
+    if (!nv) return;
+    if (wave < steps) tail_load(wave);
+    if (tid < 16) V[nv + tid] = 0.f;
+    if (a.v_sum) {
+      for (int o = tid; o < nv; o += NT) V[o] = a.V[o];
+      return;
+    }
+    const int nfb = a.f * a.Pin / 32, parts = NT / nv, p = tid / nv, o = tid - p * nv;
+    float x[kDownPartials];
+#pragma unroll
+    for (int i = 0; i < kDownPartials; ++i) {
+      const int b = p + i * parts;
+      x[i] = p < parts && b < nfb ? a.Vp[static_cast<long>(b) * nv + o] : 0.f;
+    }
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kDownPartials; ++i) s += x[i];
+    vpart[tid] = s;
+    __syncthreads();
+    if (tid < nv) {
+      float v = 0.f;
+      for (int i = 0; i < parts; ++i) v += vpart[i * nv + tid];
+      V[tid] = v;
     }
   };
   if constexpr (Q4) {
@@ -788,7 +988,8 @@ __global__ __launch_bounds__(NT) void few_down_kernel(FewArgs a) {
               for (int i = 0; i < 4; ++i) acc[m][i] += sc * p[i];
             }
           }
-        });
+        },
+        between);
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -814,43 +1015,25 @@ __global__ __launch_bounds__(NT) void few_down_kernel(FewArgs a) {
           for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int m = 0; m < MT; ++m) acc[m] = mfma16<TY>(raw_to_frag<TY, TY>(s.x[h][m]), s.w[h], acc[m]);
-        });
+        },
+        between);
+  }
+  if (nv) {
+    __syncthreads();  // V is in LDS
+    for (int i = wave; i < steps; i += NW) {
+      tail_use();
+      if (i + NW < steps) tail_load(i + NW);
+    }
   }
 #pragma unroll
   for (int m = 0; m < MT; ++m) *reinterpret_cast<f4v*>(red + (wave * MT + m) * 256 + lane * 4) = acc[m];
-  // residual tail: (token, slot) times 16 columns
-  for (int v = tid; v < nv; v += NT) {
-    const int c = v & 15, slot = v >> 4, e = a.idx[slot];
-    const int g = e / a.K, j = e - g * a.K, n32 = n >> 1, nl = 16 * (n & 1) + c;
-    const long sblk = (static_cast<long>(e) * (a.d / 32) + n32) * RPAD;
-    const long base = a.resid == RS_INT4 ? g * a.bd_gs : g * a.bd_gs / 8;  // in eights of values
-    float s = 0.f;
-#pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
-      // rank column 8 hh .. of expert j in the permuted depth order
-      const int ks = 4 * (j >> 2) + 2 * (j & 1) + hh, half = (j >> 1) & 1;
-      float bv[8];
-      factor8<TY>(a.resid, a.Bd, base + (static_cast<long>(n32) * (a.NV / 16) + ks) * 64 + nl + 32 * half,
-                  a.Bd_s + sblk + 8 * hh, false, bv);
-#pragma unroll
-      for (int r = 0; r < 8; ++r) s = fmaf(V[slot * 16 + 8 * hh + r], bv[r], s);
-    }
-    tail[v] = s;
-  }
   __syncthreads();
   for (int v = tid; v < a.T * 16; v += NT) {
     const int t = v >> 4, c = v & 15;
     float s = 0.f;
 #pragma unroll
-    for (int p = planes - 1; p >= 0; --p) {  // the rests first
-      const int m = packed ? 0 : planes == 1 ? t >> 4 : p * (MT / 2) + (t >> 4);
-      const int r = packed ? t + 8 * p : t & 15;
-      const int at = m * 256 + (16 * (r >> 2) + c) * 4 + (r & 3);
-#pragma unroll
-      for (int w = 0; w < NW; ++w) s += red[w * MT * 256 + at];
-    }
-    if (nv)
-      for (int i = 0; i < a.k; ++i) s += tail[(t * a.k + i) * 16 + c];
+    for (int p = planes - 1; p >= 0; --p)  // the rests first
+      s += block_sum<NW, 1, MT>(red, packed ? t + 8 * p : 16 * TM * p + t, c);
     static_cast<typename Elem<XT>::T*>(a.Y)[static_cast<long>(t) * a.d + n * 16 + c] = from_f32<XT>(s);
   }
 }
@@ -882,25 +1065,31 @@ __global__ __launch_bounds__(256) void repack_kernel(const TS* src0, const TS* s
 
 // -------------------------------------------------------------- launches --
 template <class K>
-hipError_t go(K kernel, unsigned grid, size_t lds, const FewArgs& a, hipStream_t st) {
+hipError_t go(K kernel, unsigned grid, unsigned threads, size_t lds, const FewArgs& a, hipStream_t st) {
   if (lds > 64 * 1024) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(lds));
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(kernel, dim3(grid), dim3(NT), lds, st, a);
+  hipLaunchKernelGGL(kernel, dim3(grid), dim3(threads), lds, st, a);
   return hipGetLastError();
 }
 
 template <int XT, int TY, int RS, int MT>
 hipError_t route_mt(const FewArgs& a, hipStream_t st) {
-  const unsigned nsb = (a.NCp / 32) * a.nsplit, nub = a.G * ((a.K * a.Pin * 16 + 31) / 32);
-  const size_t tiles = static_cast<size_t>(NW) * 2 * MT * 256 * sizeof(float);
-  const size_t sc = static_cast<size_t>(NW) * (a.G + (a.K > 1 ? a.G * a.K : 0)) * sizeof(float);
-  hipError_t e = go(few_route_kernel<XT, TY, RS, MT>, nsb + (RS != RS_NONE && a.u_all ? nub : 0),
-                    sc > tiles ? sc : tiles, a, st);
+  const int NC = a.G + (a.K > 1 ? a.G * a.K : 0);
+  const unsigned nsb = (NC + 15) / 16 * a.nsplit, nub = a.G * ((a.K * a.Pin * 16 + 31) / 32);
+  const size_t tiles = static_cast<size_t>(NW) * 2 * MT * 256 * sizeof(float);  // of u_block
+  const size_t scores =
+      sizeof(float) * (static_cast<size_t>(NW) * MT * 256 + static_cast<size_t>(select_chunk(a.T, NC)) * NC);
+  const size_t tables =
+      sizeof(int16_t) * FEW_MAX_T * (a.G + static_cast<size_t>(a.E < a.T * a.k ? a.E : a.T * a.k));
+  size_t lds = RS != RS_NONE && a.u_all ? tiles : 0;
+  if (scores > lds) lds = scores;
+  if (tables > lds) lds = tables;
+  hipError_t e = go(few_route_kernel<XT, TY, RS, MT>, nsb + (RS != RS_NONE && a.u_all ? nub : 0), NT, lds, a, st);
   if constexpr (RS != RS_NONE)
-    if (e == hipSuccess && !a.u_all) e = go(few_u_kernel<XT, TY, RS, MT>, nub, tiles, a, st);
+    if (e == hipSuccess && !a.u_all) e = go(few_u_kernel<XT, TY, RS, MT>, nub, NT, tiles, a, st);
   return e;
 }
 template <int XT, int TY, int RS>
@@ -908,12 +1097,18 @@ hipError_t route_rs(const FewArgs& a, hipStream_t st) {
   return a.T <= 16 ? route_mt<XT, TY, RS, 1>(a, st) : route_mt<XT, TY, RS, 2>(a, st);
 }
 
+template <int XT, int TY, bool Q4, int MT>
+hipError_t up_mt(const FewArgs& a, hipStream_t st) {
+  const unsigned grid = static_cast<unsigned>(a.G < a.T * a.kg ? a.G : a.T * a.kg) * (a.f * a.Pin / 32);
+  const size_t lds = sizeof(float) * 2 * MT * 256;  // per wavefront
+  // hw [rows][ke][FT], at most 16 MT rows
+  const size_t hw = sizeof(float) * (a.T < 16 * MT ? a.T : 16 * MT) * a.ke * (32 / a.Pin);
+  if (grid > 256) return go(few_up_kernel<XT, TY, Q4, MT, 8>, grid, 512, 8 * lds > hw ? 8 * lds : hw, a, st);
+  return go(few_up_kernel<XT, TY, Q4, MT, 16>, grid, 1024, 16 * lds > hw ? 16 * lds : hw, a, st);
+}
 template <int XT, int TY, bool Q4>
 hipError_t up_q(const FewArgs& a, hipStream_t st) {
-  const unsigned grid = static_cast<unsigned>(a.G < a.T * a.kg ? a.G : a.T * a.kg) * (a.f * a.Pin / 32);
-  const size_t lds = static_cast<size_t>(NW) * 2 * 256 * sizeof(float);
-  return a.T <= 16 ? go(few_up_kernel<XT, TY, Q4, 1>, grid, lds, a, st)
-                   : go(few_up_kernel<XT, TY, Q4, 2>, grid, 2 * lds, a, st);
+  return a.T <= 16 ? up_mt<XT, TY, Q4, 1>(a, st) : up_mt<XT, TY, Q4, 2>(a, st);
 }
 
 template <int XT, int TY, bool Q4>
@@ -921,22 +1116,36 @@ hipError_t down_q(const FewArgs& a, hipStream_t st) {
   const unsigned grid = a.d / 16;
   const int groups = a.G < a.T * a.kg ? a.G : a.T * a.kg;
   const int nv = a.resid != RS_NONE ? a.T * a.k * 16 : 0;
+  if (nv && a.v_sum) {
+    hipLaunchKernelGGL(few_vsum_kernel, dim3((nv + 63) / 64), dim3(NT), 0, st, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
   const int mt = TY == DT_F32 ? (a.T <= 16 ? 1 : 2) : a.T <= 8 ? 1 : a.T <= 16 ? 2 : 4;
-  const size_t lds = sizeof(float) * (static_cast<size_t>(NW) * mt * 256 + nv + (nv > NT ? nv : NT)) +
+  const size_t lds = sizeof(float) * (static_cast<size_t>(NW) * mt * 256 + nv + 16 + (nv && !a.v_sum ? NT : 0)) +
                      sizeof(int16_t) * groups * FEW_MAX_T;
-  if (mt == 1) return go(few_down_kernel<XT, TY, Q4, 1>, grid, lds, a, st);
-  if (mt == 2) return go(few_down_kernel<XT, TY, Q4, 2>, grid, lds, a, st);
-  if constexpr (TY != DT_F32) return go(few_down_kernel<XT, TY, Q4, 4>, grid, lds, a, st);
+  if (mt == 1) return go(few_down_kernel<XT, TY, Q4, 1>, grid, NT, lds, a, st);
+  if (mt == 2) return go(few_down_kernel<XT, TY, Q4, 2>, grid, NT, lds, a, st);
+  if constexpr (TY != DT_F32) return go(few_down_kernel<XT, TY, Q4, 4>, grid, NT, lds, a, st);
   return hipErrorInvalidValue;
 }
 
 }  // namespace
 
-int few_router_splits(int d) {
-  // two 32-deep units per wavefront keep the matrix's loads in flight; at most
-  // 8 partial scores for the selection to add
+int few_router_splits(int d, int NCp) {
+  // at most 16 columns that one workgroup reads in a few microseconds need no
+  // exchange of scores; else two 32-deep units per wavefront keep the matrix's
+  // loads in flight, with at most 4 parts for the selection to add
+  if (NCp == 32 && d <= 8192) return 1;
   const int s = d / 32 / (2 * NW);
-  return s < 1 ? 1 : s > 8 ? 8 : s;
+  return s < 1 ? 1 : s > 4 ? 4 : s;
+}
+
+bool few_v_sum(const FewArgs& a) {
+  const long nv = static_cast<long>(a.T) * a.k * 16, nfb = a.f * a.Pin / 32;
+  if (nv > NT) return true;
+  const long parts = NT / nv;
+  return (nfb + parts - 1) / parts > kDownPartials;
 }
 
 hipError_t launch_few_route(int xt, int ty, const FewArgs& a, hipStream_t st) {

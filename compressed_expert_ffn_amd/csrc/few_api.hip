@@ -42,8 +42,11 @@ int create_few(moe_handle* h) {
     s.gidx = reinterpret_cast<int*>(take(sizeof(int) * T * kg));
     s.glist = reinterpret_cast<int*>(take(sizeof(int) * (1 + c.G)));
     s.grow = reinterpret_cast<int16_t*>(take(sizeof(int16_t) * std::min<size_t>(c.G, T * kg) * FEW_MAX_T));
-    s.L = reinterpret_cast<float*>(take(sizeof(float) * few_router_splits(c.d) * T * h->NCp));
+    s.L = reinterpret_cast<float*>(take(sizeof(float) * few_router_splits(c.d, h->NCp) * T * h->NCp));
+    s.elist = reinterpret_cast<int*>(take(sizeof(int) * (1 + std::min<size_t>(h->E, T * h->k))));
+    s.eslot = reinterpret_cast<int16_t*>(take(sizeof(int16_t) * std::min<size_t>(h->E, T * h->k) * FEW_MAX_T));
     if (c.r > 0) {
+      s.V = reinterpret_cast<float*>(take(sizeof(float) * (T * h->k + 1) * RPAD));
       s.U = reinterpret_cast<float*>(take(sizeof(float) * T * h->E * h->P_in * RPAD));
       s.Vp = reinterpret_cast<float*>(take(sizeof(float) * col_blocks(h) * T * h->k * RPAD));
     }
@@ -53,7 +56,8 @@ int create_few(moe_handle* h) {
   TRY(dalloc(h, &base, off));
   carve();
   char* zero = static_cast<char*>(s.H) + hidden_row_bytes(h) * T * kg;
-  if (hipMemset(s.ticket, 0, sizeof(int)) != hipSuccess || hipMemset(zero, 0, hidden_row_bytes(h)) != hipSuccess) {
+  if (hipMemset(s.ticket, 0, sizeof(int)) != hipSuccess || hipMemset(zero, 0, hidden_row_bytes(h)) != hipSuccess ||
+      (s.V && hipMemset(s.V + T * h->k * RPAD, 0, RPAD * sizeof(float)) != hipSuccess)) {
     (void)hipGetLastError();
     return fail(MOE_ERR_HIP, "initialising the few-token workspace failed");
   }
@@ -97,7 +101,7 @@ extern "C" int moe_forward_few(moe_handle* h, const void* X, int32_t T, void* Y,
   a.act = c.act == MOE_ACT_SWIGLU ? ACT_SWIGLU : ACT_GELU;
   a.Wr = h->Wr;
   a.NCp = h->NCp;
-  a.nsplit = few_router_splits(c.d);
+  a.nsplit = few_router_splits(c.d, h->NCp);
   a.gbias = h->gbias;
   a.ebias = h->ebias;
   a.L = s.L;
@@ -141,7 +145,12 @@ extern "C" int moe_forward_few(moe_handle* h, const void* X, int32_t T, void* Y,
   a.Vp = s.Vp;
   a.H = s.H;
   a.zero_row = s.T_cap * c.top_groups;
+  a.V = s.V;
+  a.zero_slot = s.T_cap * h->k;
+  a.elist = s.elist;
+  a.eslot = s.eslot;
   hipStream_t st = static_cast<hipStream_t>(stream);
+  a.v_sum = few_v_sum(a) ? 1 : 0;
   hipError_t e = launch_few_route(c.x_dtype, h->mma, a, st);
   if (e == hipSuccess) e = launch_few_up(c.x_dtype, h->mma, q4, a, st);
   if (e == hipSuccess) e = launch_few_down(c.x_dtype, h->mma, q4, a, st);

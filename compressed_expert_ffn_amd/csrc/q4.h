@@ -81,6 +81,19 @@ __device__ __forceinline__ typename Frag<TY>::T q4_frag(uint32_t w) {
   r[3] = (__builtin_rotateright32(w, 12) & Q4Type<TY>::mask) | Q4Type<TY>::magic;
   return __builtin_bit_cast(typename Frag<TY>::T, r);
 }
+// The same of a word in the residual factors' order (code e at bits 4 e):
+// even and odd codes apart, a byte each, then byte i of both into one pair.
+template <int TY>
+__device__ __forceinline__ typename Frag<TY>::T q4_frag_plain(uint32_t w) {
+  const uint32_t even = w & 0x0F0F0F0Fu, odd = (w >> 4) & 0x0F0F0F0Fu;
+  constexpr int bit = TY == DT_F16 ? 6 : 3;
+  u4v r;
+  r[0] = (__builtin_amdgcn_perm(even, odd, 0x0c000c04u) << bit) | Q4Type<TY>::magic;
+  r[1] = (__builtin_amdgcn_perm(even, odd, 0x0c010c05u) << bit) | Q4Type<TY>::magic;
+  r[2] = (__builtin_amdgcn_perm(even, odd, 0x0c020c06u) << bit) | Q4Type<TY>::magic;
+  r[3] = (__builtin_amdgcn_perm(even, odd, 0x0c030c07u) << bit) | Q4Type<TY>::magic;
+  return __builtin_bit_cast(typename Frag<TY>::T, r);
+}
 // Eight times 1 / undo.
 template <int TY>
 __device__ __forceinline__ typename Frag<TY>::T q4_ones() {

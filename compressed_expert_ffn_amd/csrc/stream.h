@@ -12,12 +12,17 @@ namespace cefn {
 // times, from cache) so that the loop has no branches between the loads.  The
 // scheduling barriers keep one unit's decode from being hoisted over another's:
 // all units' decoded operands at once do not fit the registers.
-template <int R, class Slot, class Issue, class Use>
-__device__ __forceinline__ void stream_units(int n, Issue&& issue, Use&& use) {
-  if (n <= 0) return;
+// between() runs once the first units' loads are under way (also where n is
+// 0): what it reads arrives behind them.
+template <int R, class Slot, class Issue, class Use, class Between>
+__device__ __forceinline__ void stream_units(int n, Issue&& issue, Use&& use, Between&& between) {
   Slot ring[R];
+  if (n > 0) {
 #pragma unroll
-  for (int p = 0; p < R; ++p) issue(p < n ? p : n - 1, ring[p]);
+    for (int p = 0; p < R; ++p) issue(p < n ? p : n - 1, ring[p]);
+  }
+  __builtin_amdgcn_sched_barrier(0);
+  between();
   __builtin_amdgcn_sched_barrier(0);
   int i = 0;
   for (; i + R < n; i += R) {
@@ -36,6 +41,11 @@ __device__ __forceinline__ void stream_units(int n, Issue&& issue, Use&& use) {
       use(ring[p]);
       __builtin_amdgcn_sched_barrier(0);
     }
+}
+
+template <int R, class Slot, class Issue, class Use>
+__device__ __forceinline__ void stream_units(int n, Issue&& issue, Use&& use) {
+  stream_units<R, Slot>(n, issue, use, [] {});
 }
 
 // Eight consecutive 16-bit activations, k .. k + 7 of the row at p; from n on

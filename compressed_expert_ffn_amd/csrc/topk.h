@@ -21,8 +21,7 @@ __device__ inline void wave_topk(const float* sv, int n, int k, int lane, float&
     }
     int rank = 0;
     for (int j = 0; j < n; ++j) {
-      float u = sv[j];
-      u = (u == u) ? u : -INFINITY;
+      const float u = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), j));
       rank += (u > v || (u == v && j < lane)) ? 1 : 0;
     }
     myv = -INFINITY;
@@ -30,9 +29,9 @@ __device__ inline void wave_topk(const float* sv, int n, int k, int lane, float&
     for (int r = 0; r < k; ++r) {
       const unsigned long long m = __ballot(lane < n && rank == r);
       const int c = __ffsll((long long)m) - 1;
+      const float u = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), c));
       if (lane == r) {
-        float u = sv[c];
-        myv = (u == u) ? u : -INFINITY;
+        myv = u;
         myi = c;
       }
     }
