@@ -246,7 +246,7 @@ int upload_raw(moe_handle* h, void** dst, const std::vector<T>& src) {
 // Base weights in device memory, packed there: 16- and 32-bit ones in the same
 // order as pack_frag's, or quantised to 4 bits (q4.h; input projections in
 // tiles of 32 columns, 16 gate and 16 up for SwiGLU; output projection in
-// tiles of 16).  A host base (4-bit layers only) is sent over group by group.
+// tiles of 16, for fp16 MFMAs whatever the activations).  A host base (4-bit layers only) is sent over group by group.
 int build_base_on_device(moe_handle* h, const moe_weights* w, bool on_device) {
   const moe_config& c = h->cfg;
   const int G = c.G, P = h->P, Pin = h->P_in, d = c.d, f = c.f;
@@ -310,7 +310,7 @@ int build_base_on_device(moe_handle* h, const moe_weights* w, bool on_device) {
     if (e == hipSuccess)
       e = launch_q4_pack(s1, in, h->mma, w1 + (size_t)g * s1.words(), h->W1_s + (size_t)g * s1.scales(), nullptr);
     if (e == hipSuccess)
-      e = launch_q4_pack(s2, out, h->mma, w2 + (size_t)g * s2.words(), h->W2_s + (size_t)g * s2.scales(), nullptr);
+      e = launch_q4_pack(s2, out, MOE_F16, w2 + (size_t)g * s2.words(), h->W2_s + (size_t)g * s2.scales(), nullptr);
     if (e == hipSuccess && !on_device) e = hipDeviceSynchronize();  // before the staging buffers are reused
   }
   if (e == hipSuccess) e = hipDeviceSynchronize();

@@ -46,6 +46,7 @@ struct Workspace {
 struct FewState {
   int T_cap = 0;
   int *idx = nullptr, *gidx = nullptr, *glist = nullptr, *elist = nullptr, *ticket = nullptr;
+  int4* grec = nullptr;
   int16_t *grow = nullptr, *eslot = nullptr;
   float *w = nullptr, *L = nullptr, *U = nullptr, *Vp = nullptr, *V = nullptr;
   void* H = nullptr;

@@ -26,11 +26,14 @@ struct FewArgs {
   float* w;       // [T][k]
   int* gidx;      // [T][kg]
   int *counts, *offsets, *perm, *gcounts, *goffsets, *gperm;
-  // touched groups: glist[0] of them, glist[1 + a] the a-th (ascending), and
-  // grow[a][t] the row t*kg + rank of token t in it, or -1
+  int wants_lists;  // any of the six is asked for
+  // touched groups: glist[0] of them, grec[a] the a-th's {group, its first
+  // touched expert in elist, how many, its tokens}, and grow[a][t] the row
+  // t*kg + rank of token t in it, or -1 (rows t < T)
   int* glist;
+  int4* grec;
   int16_t* grow;  // [min(G, T*kg)][FEW_MAX_T]
-  // the same of the touched experts, for the residual tail: elist[0] of them,
+  // the touched experts, group by group, with a residual: elist[0] of them,
   // and eslot[i][t] the slot t*k + b of token t that chose expert elist[1 + i], or -1
   int* elist;
   int16_t* eslot;  // [min(E, T*k)][FEW_MAX_T]
@@ -54,7 +57,7 @@ struct FewArgs {
   float* V;       // [T*k + 1][16]: their sums (v_sum), and a row of zeros at zero_slot
   int v_sum;      // 1: summed by a launch of its own; 0: by every workgroup of the down product
   int zero_slot;
-  void* H;        // [T*kg][planes][f]: gate-weighted hidden sums, fp32 (one plane), or two 16-bit planes, value and rest
+  void* H;        // [T*kg][planes][f]: gate-weighted hidden sums, in fp32 or one or two 16-bit parts
   int zero_row;   // row of H that stays zero (the last of the workspace)
 };
 

@@ -36,6 +36,11 @@ namespace {
 constexpr int NW = FEW_WAVES;
 constexpr int NT = NW * 64;
 
+// The value a wavefront's lane r (the same for all lanes) holds.
+__device__ __forceinline__ float lane_value(float v, int r) {
+  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), r));
+}
+
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 
 // Eight consecutive activations as loaded, and as operands.
@@ -103,6 +108,75 @@ __device__ __forceinline__ void factor8(int resid, const void* base, long i8, co
   }
   constexpr int es = TY == DT_F32 ? 4 : 2;
   frag_to_f32<TY>(load_frag<TY>(static_cast<const char*>(base) + i8 * 8 * es), o);
+}
+
+// Type and 16-bit parts the gate-weighted hidden sums (and V) are held in for
+// the down product.  An fp16 number is exact to 2^-12, a sixteenth of what a
+// bf16 result is rounded by, so bf16 activations on fp16 MFMAs need one part;
+// where the result has the MFMAs' own precision the sums keep two, 22 or 16
+// bits, so that y is rounded once.  A 4-bit base takes either MFMA type, hence
+// fp16 for its down product.
+__host__ __device__ constexpr int hidden_type(int ty, bool q4) {
+  return q4 ? DT_F16 : ty;
+}
+__host__ __device__ constexpr int hidden_planes(int xt, int ht) {
+  return ht == DT_F32 || (xt == DT_BF16 && ht == DT_F16) ? 1 : 2;
+}
+
+// v + A_down^T h over 16 columns of f: lane (l, q) holds rank column l of the
+// factor at columns 4 q .. + 3 and h of its token there; lane (l, q) of v:
+// rank columns 4 q .. of token l.  h goes in as two 16-bit parts.
+typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+typedef short s4 __attribute__((ext_vector_type(4)));
+template <int TY>
+__device__ __forceinline__ f4v mfma16k16(const uint16_t (&x)[4], const uint16_t (&y)[4], f4v c) {
+  s4 p, r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    p[i] = static_cast<short>(x[i]);
+    r[i] = static_cast<short>(y[i]);
+  }
+  if constexpr (TY == DT_F16)
+    return __builtin_amdgcn_mfma_f32_16x16x16f16(__builtin_bit_cast(h4, p), __builtin_bit_cast(h4, r), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(p, r, c, 0, 0, 0);
+}
+// Its operand: four values (or the word holding four codes) of eight `at`, half `half`.
+template <int TY>
+__device__ __forceinline__ u4v load_down_factor(int resid, const void* Ad, long at, int half) {
+  u4v r = {0u, 0u, 0u, 0u};
+  if constexpr (TY == DT_F32) {
+    r = *reinterpret_cast<const u4v*>(static_cast<const float*>(Ad) + at * 8 + 4 * half);
+  } else if (resid == RS_INT4) {
+    r[0] = static_cast<const uint32_t*>(Ad)[at] >> (16 * half);
+  } else {
+    const u2v d = *reinterpret_cast<const u2v*>(static_cast<const uint16_t*>(Ad) + at * 8 + 4 * half);
+    r[0] = d[0];
+    r[1] = d[1];
+  }
+  return r;
+}
+template <int TY>
+__device__ __forceinline__ f4v down_factor(int resid, const u4v& ad, const float (&h)[4], f4v v) {
+  if constexpr (TY == DT_F32) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const uint32_t w = ad[r];
+      v = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(w), h[r], v, 0, 0, 0);
+    }
+    return v;
+  } else {
+    uint16_t w[4], hi[4], lo[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t x = ad[0], y = ad[i >> 1];
+      w[i] = resid == RS_INT4 ? from_f32<TY>(static_cast<float>(static_cast<int>((x >> (4 * i)) & 15u) - 8))
+                              : static_cast<uint16_t>((y >> (16 * (i & 1))) & 0xFFFFu);
+      hi[i] = from_f32<TY>(h[i]);
+      lo[i] = from_f32<TY>(h[i] - (TY == DT_F16 ? f16_bits_to_f32(hi[i]) : bf16_bits_to_f32(hi[i])));
+    }
+    return mfma16k16<TY>(w, lo, mfma16k16<TY>(w, hi, v));
+  }
 }
 
 // ---------------------------------------------------------------- route --
@@ -312,8 +386,8 @@ struct SelectLds {
   int last;
 };
 
-// Position of each non-zero count among the non-zero ones (id order), by all
-// threads for up to NT counts; returns their number.
+// Number of non-zero counts before each id (a non-zero one's position among
+// them), by all threads for up to NT counts; returns how many there are.
 __device__ int compact(const int* count, int n, int* pos, int* wsum) {
   const int tid = threadIdx.x, wave = wave_id(), lane = tid & 63;
   const bool on = tid < n && count[tid] > 0;
@@ -327,7 +401,7 @@ __device__ int compact(const int* count, int n, int* pos, int* wsum) {
     before += w < wave ? c : 0;
     total += c;
   }
-  if (on) pos[tid] = before + __popcll(m & ((1ull << lane) - 1));
+  if (tid < n) pos[tid] = before + __popcll(m & ((1ull << lane) - 1));
   __syncthreads();
   return total;
 }
@@ -369,9 +443,9 @@ __device__ void select_tokens(const FewArgs& a, int t0, int nt, int NC, const fl
     float v;
     int g;
     wave_topk(sc + i * NC, a.G, a.kg, lane, v, g);
-    const float e = lane < a.kg ? expf(v - __shfl(v, 0)) : 0.f;
+    const float e = lane < a.kg ? expf(v - lane_value(v, 0)) : 0.f;
     float sum = 0.f;
-    for (int r = 0; r < a.kg; ++r) sum += __shfl(e, r);
+    for (int r = 0; r < a.kg; ++r) sum += lane_value(e, r);
     if (lane < a.kg) {
       s.gid[t * a.kg + lane] = g;
       s.pg[t * a.kg + lane] = e / sum;
@@ -390,9 +464,9 @@ __device__ void select_tokens(const FewArgs& a, int t0, int nt, int NC, const fl
     float v;
     int j;
     wave_topk(sc + (i / a.kg) * NC + a.G + g * a.K, a.K, a.ke, lane, v, j);
-    const float e = lane < a.ke ? expf(v - __shfl(v, 0)) : 0.f;
+    const float e = lane < a.ke ? expf(v - lane_value(v, 0)) : 0.f;
     float sum = 0.f;
-    for (int r = 0; r < a.ke; ++r) sum += __shfl(e, r);
+    for (int r = 0; r < a.ke; ++r) sum += lane_value(e, r);
     if (lane < a.ke) {
       const int slot = tr * a.ke + lane;  // (t * kg + rank) * ke + b
       s.idx[slot] = g * a.K + j;
@@ -408,31 +482,55 @@ __device__ void select_tokens(const FewArgs& a, int t0, int nt, int NC, const fl
 __device__ void make_lists(const FewArgs& a, SelectLds& s, int16_t* tab) {
   const int tid = threadIdx.x;
   const int ng = a.T * a.kg, na = a.T * a.k;
+  const bool resid = a.resid != RS_NONE;
+  // one token: its groups and experts are distinct and in place already
+  const bool one = a.T == 1;
+  if (one) {
+    if (tid == 0) a.glist[0] = ng;
+    if (tid < ng) {
+      a.grec[tid] = int4{s.gid[tid], tid * a.ke, a.ke, 1};
+      a.grow[tid * FEW_MAX_T] = static_cast<int16_t>(tid);
+    }
+    if (resid) {
+      if (tid == 0) a.elist[0] = na;
+      if (tid < na) {
+        a.elist[1 + tid] = s.idx[tid];
+        a.eslot[tid * FEW_MAX_T] = static_cast<int16_t>(tid);
+      }
+    }
+    if (!a.wants_lists) return;
+  }
   if (tid < a.G) s.gcount[tid] = 0;
   if (tid < a.E) s.ecount[tid] = 0;
   __syncthreads();
   if (tid < ng) atomicAdd(&s.gcount[s.gid[tid]], 1);
   if (tid < na) atomicAdd(&s.ecount[s.idx[tid]], 1);
   __syncthreads();
-  const int tg = compact(s.gcount, a.G, s.gpos, s.wsum);
-  const int te = a.resid != RS_NONE ? compact(s.ecount, a.E, s.epos, s.wsum) : 0;
-  int16_t* etab = tab + a.G * FEW_MAX_T;
-  for (int i = tid; i < tg * (FEW_MAX_T / 2); i += NT) reinterpret_cast<int*>(tab)[i] = -1;
-  for (int i = tid; i < te * (FEW_MAX_T / 2); i += NT) reinterpret_cast<int*>(etab)[i] = -1;
-  __syncthreads();
-  if (tid < ng) tab[s.gpos[s.gid[tid]] * FEW_MAX_T + tid / a.kg] = static_cast<int16_t>(tid);
-  if (te && tid < na) etab[s.epos[s.idx[tid]] * FEW_MAX_T + tid / a.k] = static_cast<int16_t>(tid);
-  if (tid == 0) a.glist[0] = tg;
-  if (tid < a.G && s.gcount[tid] > 0) a.glist[1 + s.gpos[tid]] = tid;
-  if (te) {
-    if (tid == 0) a.elist[0] = te;
-    if (tid < a.E && s.ecount[tid] > 0) a.elist[1 + s.epos[tid]] = tid;
+  if (!one) {
+    const int tg = compact(s.gcount, a.G, s.gpos, s.wsum);
+    const int te = resid ? compact(s.ecount, a.E, s.epos, s.wsum) : 0;
+    int16_t* etab = tab + a.G * FEW_MAX_T;
+    for (int i = tid; i < tg * (FEW_MAX_T / 2); i += NT) reinterpret_cast<int*>(tab)[i] = -1;
+    for (int i = tid; i < te * (FEW_MAX_T / 2); i += NT) reinterpret_cast<int*>(etab)[i] = -1;
+    if (tid == 0) a.glist[0] = tg;
+    if (tid < a.G && s.gcount[tid] > 0) {
+      const int first = resid ? s.epos[tid * a.K] : 0, end = !resid ? 0 : tid + 1 < a.G ? s.epos[(tid + 1) * a.K] : te;
+      a.grec[s.gpos[tid]] = int4{tid, first, end - first, s.gcount[tid]};
+    }
+    if (resid) {
+      if (tid == 0) a.elist[0] = te;
+      if (tid < a.E && s.ecount[tid] > 0) a.elist[1 + s.epos[tid]] = tid;
+    }
+    __syncthreads();
+    if (tid < ng) tab[s.gpos[s.gid[tid]] * FEW_MAX_T + tid / a.kg] = static_cast<int16_t>(tid);
+    if (te && tid < na) etab[s.epos[s.idx[tid]] * FEW_MAX_T + tid / a.k] = static_cast<int16_t>(tid);
+    __syncthreads();
+    for (int i = tid; i < tg * (FEW_MAX_T / 2); i += NT)
+      reinterpret_cast<int*>(a.grow)[i] = reinterpret_cast<const int*>(tab)[i];
+    for (int i = tid; i < te * (FEW_MAX_T / 2); i += NT)
+      reinterpret_cast<int*>(a.eslot)[i] = reinterpret_cast<const int*>(etab)[i];
   }
-  __syncthreads();
-  for (int i = tid; i < tg * (FEW_MAX_T / 2); i += NT)
-    reinterpret_cast<int*>(a.grow)[i] = reinterpret_cast<const int*>(tab)[i];
-  for (int i = tid; i < te * (FEW_MAX_T / 2); i += NT)
-    reinterpret_cast<int*>(a.eslot)[i] = reinterpret_cast<const int*>(etab)[i];
+  if (!a.wants_lists) return;
   // the caller's lists: an entry's place in its bin's list is the entries of
   // lower bins and those before it in its own (tokens ascend within a bin)
   if (a.gcounts && tid < a.G) a.gcounts[tid] = s.gcount[tid];
@@ -557,21 +655,69 @@ template <int XT, int TY, bool Q4, int MT, int NWV>
 __global__ __launch_bounds__(NWV * 64) void few_up_kernel(FewArgs a) {
   using XE = typename Elem<XT>::T;
   using B = typename Frag<TY>::T;
-  extern __shared__ __attribute__((aligned(16))) float red[];  // partial tiles, then hw [rows][ke][FT]
-  __shared__ float z[2][MT * 16][16];
+  constexpr int HT = hidden_type(TY, Q4);
+  extern __shared__ __attribute__((aligned(16))) float red[];  // partial tiles, then the wavefronts' hidden sums
+  __shared__ __attribute__((aligned(16))) float z[2][MT * 16][20];  // 20: rows 16 bytes apart mod 128
   __shared__ int srow[FEW_MAX_T];   // (token << 16) | row t*kg + rank, of the group's tokens
-  __shared__ int nrows;
   const int Pin = a.Pin, FT = 32 / Pin, nfb = a.f / FT;
   const int ga = blockIdx.x / nfb, fb = blockIdx.x % nfb;
   if (ga >= a.glist[0]) return;
-  const int g = a.glist[1 + ga];
+  const int4 rec = a.grec[ga];
+  const int g = rec.x, first = rec.y, ne = rec.z, n = rec.w;
   const int wave = wave_id(), lane = threadIdx.x & 63, l = lane & 15, q = lane >> 4;
+  const int f0 = fb * FT;
+  // the group's tokens
   if (wave == 0) {
     const int row = lane < a.T ? a.grow[ga * FEW_MAX_T + lane] : -1;
     const unsigned long long m = __ballot(row >= 0);
     if (row >= 0) srow[__popcll(m & ((1ull << lane) - 1))] = (lane << 16) | row;
-    if (lane == 0) nrows = __popcll(m);
   }
+  // The wavefront's jobs: (touched expert, tile of 16 tokens), expert first +
+  // wave, + NWV, ...  Their operands are few but cold, and behind a stream
+  // that fills the memory's queues a load takes microseconds: the first job's
+  // are read with the first weights, the next one's while a job runs.
+  struct Job {
+    int slot;
+    float wgt;
+    u4v b[2][TY == DT_F32 ? 2 : 1], s[2], ad[2];
+    u2v as;
+  } job;
+  int je = 0, jslot = -1;  // expert, and the slot of the lane's token
+  auto job_find = [&](int j) {
+    const int i = first + j / MT, t = 16 * (j % MT) + l;
+    je = a.elist[1 + i];
+    jslot = t < a.T ? a.eslot[i * FEW_MAX_T + t] : -1;
+  };
+  auto job_load = [&](Job& J) {
+    J.slot = jslot;
+    J.wgt = a.w[max(jslot, 0)];
+    constexpr int es = TY == DT_F32 ? 4 : 2;
+    const bool int4r = a.resid == RS_INT4;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int p = Pin == 2 ? x : 0, col0 = Pin == 2 ? f0 : f0 + 16 * x;  // 16 columns of projection p
+      const long blk = static_cast<long>(je * Pin + p) * (a.f / 32) + (col0 >> 5);
+      const long at = blk * 64 + 32 * (q & 1) + (col0 & 16) + l;
+      if (int4r) {
+        J.b[x][0][0] = static_cast<const uint32_t*>(a.B1)[at];
+        J.s[x] = *reinterpret_cast<const u4v*>(a.B1_s + blk * RPAD + 8 * (q & 1));
+      } else {
+        const u4v* bp = reinterpret_cast<const u4v*>(static_cast<const char*>(a.B1) + at * 8 * es);
+        J.b[x][0] = bp[0];
+        if constexpr (TY == DT_F32) J.b[x][1] = bp[1];
+      }
+      const int c0 = Pin == 2 ? f0 : col0;
+      const long ad = ((static_cast<long>(je) * (a.f / 32) + (c0 >> 5)) * 2 + ((c0 >> 4) & 1)) * 64 + l + 32 * (q & 1);
+      if (Pin == 1 || x == 0) J.ad[x] = load_down_factor<TY>(a.resid, a.Ad, ad, q >> 1);
+    }
+    if (int4r)
+      J.as = *reinterpret_cast<const u2v*>(a.Ad_s + (static_cast<long>(je) * (a.f / 32) + (f0 >> 5)) * RPAD + 4 * q);
+  };
+  const int jobs = a.resid != RS_NONE ? ne * MT : 0;
+  if (wave < jobs) job_find(wave);
+  auto between = [&]() {
+    if (wave < jobs) job_load(job);
+  };
   const int n64 = a.d / 64;
   const int u0 = n64 * wave / NWV, u1 = n64 * (wave + 1) / NWV;
   const XE* xp[MT];
@@ -629,7 +775,8 @@ __global__ __launch_bounds__(NWV * 64) void few_up_kernel(FewArgs a) {
               }
             }
           }
-        });
+        },
+        between);
 #pragma unroll
     for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -670,7 +817,8 @@ __global__ __launch_bounds__(NWV * 64) void few_up_kernel(FewArgs a) {
 #pragma unroll
               for (int c = 0; c < 2; ++c) acc[c][m] = mfma16<TY>(x, s.w[h][c], acc[c][m]);
             }
-        });
+        },
+        between);
   }
 #pragma unroll
   for (int c = 0; c < 2; ++c)
@@ -682,77 +830,139 @@ __global__ __launch_bounds__(NWV * 64) void few_up_kernel(FewArgs a) {
     const int row = v >> 5, col = v & 31;
     z[col >> 4][row][col & 15] = block_sum<NWV, 2, MT>(red, row, col);
   }
-  __syncthreads();  // partial tiles are read: red becomes hw
-  float* hw = red;
-  const int f0 = fb * FT, n = nrows;
-  for (int v = threadIdx.x; v < n * a.ke * FT; v += NWV * 64) {
-    const int c = v % FT, b = (v / FT) % a.ke, i = v / (FT * a.ke);
-    const int t = srow[i] >> 16, row = srow[i] & 0xFFFF;
-    const int slot = t * a.k + (row - t * a.kg) * a.ke + b;
-    const int e = a.idx[slot];
-    const float wgt = a.w[slot];
-    float zz[2];
-    zz[0] = Pin == 2 ? z[0][t][c] : z[c >> 4][t][c & 15];
-    zz[1] = Pin == 2 ? z[1][t][c] : 0.f;
-    if (a.resid != RS_NONE) {
-      const int col = f0 + c, n32 = col >> 5, nl = col & 31;
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        if (p >= Pin) break;
-        const float* u = a.U + (static_cast<long>(t) * a.E + e) * Pin * 16 + p * 16;
-        const long blk = static_cast<long>(e * Pin + p) * (a.f / 32) + n32;
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          float bv[8];
-          factor8<TY>(a.resid, a.B1, blk * 64 + 32 * hh + nl, a.B1_s + blk * RPAD + 8 * hh, false, bv);
-#pragma unroll
-          for (int r = 0; r < 8; ++r) zz[p] = fmaf(u[8 * hh + r], bv[r], zz[p]);
-        }
-      }
-    }
-    const float h = a.act == ACT_SWIGLU ? silu_f(zz[0]) * zz[1] : gelu_tanh_f(zz[0]);
-    hw[v] = wgt * h;
-  }
-  __syncthreads();
-  constexpr int planes = TY == DT_F32 ? 1 : 2;
-  for (int v = threadIdx.x; v < n * FT; v += NWV * 64) {
-    const int c = v % FT, i = v / FT;
-    const int row = srow[i] & 0xFFFF;
-    float s = 0.f;
-    for (int b = 0; b < a.ke; ++b) s += hw[(i * a.ke + b) * FT + c];
+  __syncthreads();  // the partial tiles are read: red is free again
+  constexpr int planes = hidden_planes(XT, HT);
+  auto store_hidden = [&](int row, int c, float s) {
     const long at = static_cast<long>(row) * planes * a.f + f0 + c;
-    if constexpr (TY == DT_F32) {
+    if constexpr (HT == DT_F32) {
       static_cast<float*>(a.H)[at] = s;
     } else {
-      // two 16-bit parts: the rounded value and what it leaves
-      const uint16_t hi = from_f32<TY>(s);
-      const float back = TY == DT_F16 ? f16_bits_to_f32(hi) : bf16_bits_to_f32(hi);
+      const uint16_t hi = from_f32<HT>(s);
       static_cast<uint16_t*>(a.H)[at] = hi;
-      static_cast<uint16_t*>(a.H)[at + a.f] = from_f32<TY>(s - back);
-    }
-  }
-  if (a.resid != RS_NONE) {
-    const int f32 = f0 >> 5, st0 = (f0 >> 4) & 1;
-    for (int v = threadIdx.x; v < n * a.ke * 16; v += NWV * 64) {
-      const int rho = v & 15, ib = v >> 4, i = ib / a.ke, b = ib - i * a.ke;
-      const int t = srow[i] >> 16, row = srow[i] & 0xFFFF;
-      const int slot = t * a.k + (row - t * a.kg) * a.ke + b;
-      const int e = a.idx[slot];
-      const float* hp = hw + ib * FT;
-      const long blk = static_cast<long>(e) * (a.f / 32) + f32;
-      float s = 0.f;
-      for (int j = 0; j < FT / 16; ++j) {
-        const int st = st0 + j;
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          float av[8];
-          factor8<TY>(a.resid, a.Ad, (blk * 2 + st) * 64 + rho + 32 * hh, a.Ad_s + blk * RPAD + rho, true, av);
-#pragma unroll
-          for (int x = 0; x < 8; ++x) s = fmaf(hp[16 * j + 4 * hh + (x < 4 ? x : x + 4)], av[x], s);
-        }
+      if constexpr (planes == 2) {
+        const float back = HT == DT_F16 ? f16_bits_to_f32(hi) : bf16_bits_to_f32(hi);
+        static_cast<uint16_t*>(a.H)[at + a.f] = from_f32<HT>(s - back);
       }
-      a.Vp[(static_cast<long>(fb) * a.T * a.k + slot) * 16 + rho] = s;
     }
+  };
+  if (a.resid == RS_NONE) {
+    // the group's experts are its base: one activation, their gates summed
+    for (int v = threadIdx.x; v < n * FT; v += NWV * 64) {
+      const int c = v % FT, i = v / FT;
+      const int t = srow[i] >> 16, row = srow[i] & 0xFFFF;
+      float wgt = 0.f;
+      for (int b = 0; b < a.ke; ++b) wgt += a.w[row * a.ke + b];
+      const float h = a.act == ACT_SWIGLU ? silu_f(z[0][t][c]) * z[1][t][c] : gelu_tanh_f(z[c >> 4][t][c & 15]);
+      store_hidden(row, c, wgt * h);
+    }
+    return;
+  }
+  // The group's touched experts, one (expert, tile of tokens) at a time per
+  // wavefront, everything transposed: MFMA rows are the 16 columns of f, MFMA
+  // columns the tokens.  z + B u: depth 32 = the 16 rank columns twice, against
+  // the two 16-bit parts of u (4-bit B: codes, the scales in u).  The result's
+  // lane holds 4 columns of f of its token, which is the operand form of
+  // 16x16x16 MFMAs, so h goes into V = A_down^T h (16 rank columns by tokens)
+  // from the registers, again in two parts.
+  float hsum[MT][2][4];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) hsum[m][x][r] = 0.f;
+  for (int j = wave; j < jobs; j += NWV) {
+    const int mt = j % MT, e = je, t = 16 * mt + l;
+    const Job J = job;
+    // u, then the next job's operands behind it
+    float u[2][8];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const float* up =
+          a.U + (static_cast<long>(min(t, a.T - 1)) * a.E + e) * Pin * 16 + (Pin == 2 ? x : 0) * 16 + 8 * (q & 1);
+      const f4v u0 = *reinterpret_cast<const f4v*>(up), u1 = *reinterpret_cast<const f4v*>(up + 4);
+#pragma unroll
+      for (int r = 0; r < 8; ++r) u[x][r] = r < 4 ? u0[r] : u1[r - 4];
+    }
+    if (j + NWV < jobs) {
+      job_find(j + NWV);
+      job_load(job);
+    }
+    if (!__any(J.slot >= 0)) continue;
+    const int part = q >> 1;
+    float hv[2][4];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      B bw;
+      if constexpr (TY == DT_F32) {
+        Raw<DT_F32> r;
+        r.v[0] = J.b[x][0];
+        r.v[1] = J.b[x][1];
+        bw = raw_to_frag<DT_F32, DT_F32>(r);
+      } else if (a.resid == RS_INT4) {
+        const uint32_t word = J.b[x][0][0];
+        bw = int4_frag_1scale<TY>(word, 0x3C00);  // the codes themselves
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          const uint32_t w = J.s[x][r >> 1];
+          u[x][r] *= f16_bits_to_f32(static_cast<uint16_t>((w >> (16 * (r & 1))) & 0xFFFFu));
+        }
+      } else {
+        bw = __builtin_bit_cast(B, J.b[x][0]);
+      }
+      B bu = to_frag<TY>(u[x]);
+      if constexpr (TY == DT_F32) {
+        if (part) bu = zero_frag<TY>();
+      } else {
+        float rest[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) rest[r] = u[x][r] - static_cast<float>(bu[r]);
+        const u4v hi = __builtin_bit_cast(u4v, bu), lo = __builtin_bit_cast(u4v, to_frag<TY>(rest));
+        bu = __builtin_bit_cast(B, part ? lo : hi);
+      }
+      const f4v zz = mfma16<TY>(bw, bu, *reinterpret_cast<const f4v*>(&z[x][t][4 * q]));
+#pragma unroll
+      for (int r = 0; r < 4; ++r) hv[x][r] = zz[r];
+    }
+    // a token without the expert keeps nothing of what its lane computed
+    f4v v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      if (Pin == 2 && x == 1) break;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float h = Pin == 2 ? silu_f(hv[0][r]) * hv[1][r] : gelu_tanh_f(hv[x][r]);
+        hv[x][r] = J.slot >= 0 ? J.wgt * h : 0.f;
+#pragma unroll
+        for (int m = 0; m < MT; ++m) hsum[m][x][r] += m == mt ? hv[x][r] : 0.f;
+      }
+      v = down_factor<TY>(a.resid, J.ad[x], hv[x], v);
+    }
+    if (a.resid == RS_INT4) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[r] *= scale_at(J.as, r);
+    }
+    if (J.slot >= 0) *reinterpret_cast<f4v*>(a.Vp + (static_cast<long>(fb) * a.T * a.k + J.slot) * 16 + 4 * q) = v;
+  }
+  // sum over the wavefronts' experts: [wave][m][16 tokens][FT columns]
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      if (Pin == 2 && x == 1) break;
+      f4v o;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) o[r] = hsum[m][x][r];
+      *reinterpret_cast<f4v*>(red + ((wave * MT + m) * 16 + l) * FT + 16 * x + 4 * q) = o;
+    }
+  __syncthreads();
+  for (int v = threadIdx.x; v < n * FT; v += NWV * 64) {
+    const int c = v % FT, i = v / FT;
+    const int t = srow[i] >> 16, row = srow[i] & 0xFFFF;
+    float s = 0.f;
+    const int used = min(jobs, NWV);
+    for (int w = 0; w < used; ++w) s += red[((w * MT + (t >> 4)) * 16 + (t & 15)) * FT + c];
+    store_hidden(row, c, s);
   }
 }
 
@@ -796,7 +1006,7 @@ constexpr int kDownPartials = 16;  // partials of V a thread holds in registers
 template <int XT, int TY, bool Q4, int MT>
 __global__ __launch_bounds__(NT) void few_down_kernel(FewArgs a) {
   using B = typename Frag<TY>::T;
-  extern __shared__ __attribute__((aligned(16))) float red[];  // [NW][MT][256], then V and a zero row, partials, grow
+  extern __shared__ __attribute__((aligned(16))) float red[];  // [NW][MT][256], V and a zero row, partials, grow
   const int n = blockIdx.x, nv = a.resid != RS_NONE ? a.T * a.k * 16 : 0;
   float* V = red + NW * MT * 256;
   float* vpart = V + nv + 16;
@@ -806,7 +1016,7 @@ __global__ __launch_bounds__(NT) void few_down_kernel(FewArgs a) {
   for (int i = tid; i < ng * (FEW_MAX_T / 2); i += NT)
     reinterpret_cast<int*>(grow)[i] = reinterpret_cast<const int*>(a.grow)[i];
   __syncthreads();
-  constexpr int planes = TY == DT_F32 ? 1 : 2;
+  constexpr int planes = hidden_planes(XT, TY);
   constexpr int UNIT = Q4 ? 128 : 64, NS = UNIT / 32;
   constexpr bool packed = planes == 2 && MT == 1;
   constexpr int TM = planes == 1 ? MT : MT > 1 ? MT / 2 : 1;  // tiles of tokens
@@ -825,7 +1035,7 @@ __global__ __launch_bounds__(NT) void few_down_kernel(FewArgs a) {
   const uint16_t* sp = nullptr;
   constexpr int es = TY == DT_F32 ? 4 : 2;
   auto enter = [&]() {
-    const int g = a.glist[1 + ga];
+    const int g = a.grec[ga].x;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       const int t = packed ? (l & 7) : 16 * (m % TM) + l, plane = packed ? l >> 3 : m / TM;
@@ -852,34 +1062,42 @@ __global__ __launch_bounds__(NT) void few_down_kernel(FewArgs a) {
       enter();
     }
   };
-  // the residual tail: steps of two touched experts, dealt to the wavefronts
+  // the residual tail: steps of two touched experts, dealt to the wavefronts;
+  // a wavefront's first step is read with its first weights
   const int te = nv ? a.elist[0] : 0, steps = (te + 1) / 2;
   struct Tail {
     u4v w[TY == DT_F32 ? 2 : 1], s;
     int slot[TM];
   } tail;
-  auto tail_load = [&](int i) {
-    const int ei = min(2 * i + (q >> 1), te - 1), hh = q & 1;
-    const int e = a.elist[1 + ei], g = e / a.K, j = e - g * a.K, n32 = n >> 1;
+  int te_id = 0, te_slot[TM];
+  auto tail_find = [&](int i) {
+    const int ei = 2 * i + (q >> 1);
+    te_id = a.elist[1 + min(ei, te - 1)];
+#pragma unroll
+    for (int m = 0; m < TM; ++m) {
+      const int t = packed ? (l & 7) : 16 * m + l;
+      const int slot = t < a.T && ei < te ? a.eslot[ei * FEW_MAX_T + t] : -1;
+      te_slot[m] = slot < 0 ? a.T * a.k : slot;  // the row of zeros
+    }
+  };
+  auto tail_load = [&](Tail& T) {
+    const int e = te_id, g = e / a.K, j = e - g * a.K, n32 = n >> 1, hh = q & 1;
     // rank column 8 hh .. of expert j in the permuted depth order
     const int ks = 4 * (j >> 2) + 2 * (j & 1) + hh;
     const long at = (static_cast<long>(n32) * (a.NV / 16) + ks) * 64 + 16 * (n & 1) + l + 32 * ((j >> 1) & 1);
     if (a.resid == RS_INT4) {
-      tail.w[0][0] = static_cast<const uint32_t*>(a.Bd)[g * a.bd_gs + at];
-      tail.s = *reinterpret_cast<const u4v*>(a.Bd_s + (static_cast<long>(e) * (a.d / 32) + n32) * RPAD + 8 * hh);
+      T.w[0][0] = static_cast<const uint32_t*>(a.Bd)[g * a.bd_gs + at];
+      T.s = *reinterpret_cast<const u4v*>(a.Bd_s + (static_cast<long>(e) * (a.d / 32) + n32) * RPAD + 8 * hh);
     } else {
       const u4v* p = reinterpret_cast<const u4v*>(static_cast<const char*>(a.Bd) + (g * a.bd_gs + at * 8) * es);
-      tail.w[0] = p[0];
-      if constexpr (TY == DT_F32) tail.w[1] = p[1];
+      T.w[0] = p[0];
+      if constexpr (TY == DT_F32) T.w[1] = p[1];
     }
 #pragma unroll
-    for (int m = 0; m < TM; ++m) {
-      const int t = packed ? (l & 7) : 16 * m + l;
-      const int slot = t < a.T && 2 * i + (q >> 1) < te ? a.eslot[ei * FEW_MAX_T + t] : -1;
-      tail.slot[m] = slot < 0 ? a.T * a.k : slot;  // the row of zeros
-    }
+    for (int m = 0; m < TM; ++m) T.slot[m] = te_slot[m];
   };
-  auto tail_use = [&]() {
+  if (wave < steps) tail_find(wave);
+  auto tail_use = [&](const Tail& tail) {
     B b;
     if constexpr (TY == DT_F32) {
       Raw<DT_F32> r;
@@ -921,11 +1139,11 @@ __global__ __launch_bounds__(NT) void few_down_kernel(FewArgs a) {
       }
     }
   };
-  // once the weights are under way: V into LDS (from the sum's launch, or
-  // summed here in an order set by T, k and f alone), the first tail step's loads
+  // once the weights are under way: the first tail step, and V into LDS (from
+  // the sum's launch, or summed here in an order set by T, k and f alone)
   auto between = [&]() {
     if (!nv) return;
-    if (wave < steps) tail_load(wave);
+    if (wave < steps) tail_load(tail);
     if (tid < 16) V[nv + tid] = 0.f;
     if (a.v_sum) {
       for (int o = tid; o < nv; o += NT) V[o] = a.V[o];
@@ -1021,8 +1239,12 @@ __global__ __launch_bounds__(NT) void few_down_kernel(FewArgs a) {
   if (nv) {
     __syncthreads();  // V is in LDS
     for (int i = wave; i < steps; i += NW) {
-      tail_use();
-      if (i + NW < steps) tail_load(i + NW);
+      const Tail now = tail;
+      if (i + NW < steps) {
+        tail_find(i + NW);
+        tail_load(tail);
+      }
+      tail_use(now);
     }
   }
 #pragma unroll
@@ -1101,10 +1323,8 @@ template <int XT, int TY, bool Q4, int MT>
 hipError_t up_mt(const FewArgs& a, hipStream_t st) {
   const unsigned grid = static_cast<unsigned>(a.G < a.T * a.kg ? a.G : a.T * a.kg) * (a.f * a.Pin / 32);
   const size_t lds = sizeof(float) * 2 * MT * 256;  // per wavefront
-  // hw [rows][ke][FT], at most 16 MT rows
-  const size_t hw = sizeof(float) * (a.T < 16 * MT ? a.T : 16 * MT) * a.ke * (32 / a.Pin);
-  if (grid > 256) return go(few_up_kernel<XT, TY, Q4, MT, 8>, grid, 512, 8 * lds > hw ? 8 * lds : hw, a, st);
-  return go(few_up_kernel<XT, TY, Q4, MT, 16>, grid, 1024, 16 * lds > hw ? 16 * lds : hw, a, st);
+  if (grid > 256) return go(few_up_kernel<XT, TY, Q4, MT, 8>, grid, 512, 8 * lds, a, st);
+  return go(few_up_kernel<XT, TY, Q4, MT, 16>, grid, 1024, 16 * lds, a, st);
 }
 template <int XT, int TY, bool Q4>
 hipError_t up_q(const FewArgs& a, hipStream_t st) {
@@ -1121,12 +1341,13 @@ hipError_t down_q(const FewArgs& a, hipStream_t st) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  const int mt = TY == DT_F32 ? (a.T <= 16 ? 1 : 2) : a.T <= 8 ? 1 : a.T <= 16 ? 2 : 4;
+  constexpr int planes = hidden_planes(XT, TY);
+  const int mt = planes == 1 ? (a.T <= 16 ? 1 : 2) : a.T <= 8 ? 1 : a.T <= 16 ? 2 : 4;
   const size_t lds = sizeof(float) * (static_cast<size_t>(NW) * mt * 256 + nv + 16 + (nv && !a.v_sum ? NT : 0)) +
                      sizeof(int16_t) * groups * FEW_MAX_T;
   if (mt == 1) return go(few_down_kernel<XT, TY, Q4, 1>, grid, NT, lds, a, st);
   if (mt == 2) return go(few_down_kernel<XT, TY, Q4, 2>, grid, NT, lds, a, st);
-  if constexpr (TY != DT_F32) return go(few_down_kernel<XT, TY, Q4, 4>, grid, NT, lds, a, st);
+  if constexpr (planes == 2) return go(few_down_kernel<XT, TY, Q4, 4>, grid, NT, lds, a, st);
   return hipErrorInvalidValue;
 }
 
@@ -1178,12 +1399,13 @@ hipError_t launch_few_up(int xt, int ty, bool q4, const FewArgs& a, hipStream_t 
 }
 
 hipError_t launch_few_down(int xt, int ty, bool q4, const FewArgs& a, hipStream_t st) {
+  ty = hidden_type(ty, q4);
   switch (xt * 8 + ty * 2 + (q4 ? 1 : 0)) {
     case 0: return down_q<DT_F32, DT_F32, false>(a, st);
     case 8 + 2: return down_q<DT_F16, DT_F16, false>(a, st);
     case 8 + 3: return down_q<DT_F16, DT_F16, true>(a, st);
     case 16 + 4: return down_q<DT_BF16, DT_BF16, false>(a, st);
-    case 16 + 5: return down_q<DT_BF16, DT_BF16, true>(a, st);
+    case 16 + 3: return down_q<DT_BF16, DT_F16, true>(a, st);
     case 16 + 2: return down_q<DT_BF16, DT_F16, false>(a, st);
   }
   return hipErrorInvalidValue;

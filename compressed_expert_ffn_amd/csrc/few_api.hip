@@ -13,7 +13,12 @@ namespace {
 
 int col_blocks(const moe_handle* h) { return h->cfg.f * h->P_in / 32; }
 
-size_t hidden_row_bytes(const moe_handle* h) { return 4 * (size_t)h->cfg.f; }  // fp32, or two 16-bit planes
+// A row of H: fp32, or one or two 16-bit parts (few.hip's hidden_planes).
+size_t hidden_row_bytes(const moe_handle* h) {
+  const moe_config& c = h->cfg;
+  const bool one = c.x_dtype == MOE_BF16 && c.base_dtype != MOE_BF16;
+  return (one ? 2 : 4) * (size_t)c.f;
+}
 
 }  // namespace
 
@@ -40,7 +45,8 @@ int create_few(moe_handle* h) {
     s.idx = reinterpret_cast<int*>(take(sizeof(int) * T * h->k));
     s.w = reinterpret_cast<float*>(take(sizeof(float) * T * h->k));
     s.gidx = reinterpret_cast<int*>(take(sizeof(int) * T * kg));
-    s.glist = reinterpret_cast<int*>(take(sizeof(int) * (1 + c.G)));
+    s.glist = reinterpret_cast<int*>(take(sizeof(int)));
+    s.grec = reinterpret_cast<int4*>(take(sizeof(int4) * std::min<size_t>(c.G, T * kg)));
     s.grow = reinterpret_cast<int16_t*>(take(sizeof(int16_t) * std::min<size_t>(c.G, T * kg) * FEW_MAX_T));
     s.L = reinterpret_cast<float*>(take(sizeof(float) * few_router_splits(c.d, h->NCp) * T * h->NCp));
     s.elist = reinterpret_cast<int*>(take(sizeof(int) * (1 + std::min<size_t>(h->E, T * h->k))));
@@ -116,8 +122,10 @@ extern "C" int moe_forward_few(moe_handle* h, const void* X, int32_t T, void* Y,
     a.gcounts = routing->gcounts;
     a.goffsets = routing->goffsets;
     a.gperm = routing->gperm;
+    a.wants_lists = a.counts || a.offsets || a.perm || a.gcounts || a.goffsets || a.gperm;
   }
   a.glist = s.glist;
+  a.grec = s.grec;
   a.grow = s.grow;
   a.At = h->At;
   a.At_s = h->At_s;

@@ -12,6 +12,16 @@ for fp16, 2^-17 for bf16, times the root of f <= 2^10 in the result: under
 2^-12), i.e. at most a twentieth of eps / 2 for fp16 and bf16; in norm and, for
 single values, of the largest.  fp32 layers keep the library's bar of 1e-5 of
 the largest value.
+
+bf16 activations on fp16 MFMAs (an fp16 or 4-bit base) hold each hidden sum h
+(and each rank sum) as one fp16 number, off by at most 2^-11 |h|, evenly
+distributed: standard deviation 2^-11 / sqrt(3) |h| at most.  Those errors are
+independent, so y = sum h w is off by a standard deviation of 2^-11 / sqrt(3)
+sqrt(sum h^2 w^2), and with weights of one variance sqrt(sum h^2 w^2) is the
+root mean square of the token's y.  Six of these, 6 / sqrt(3) 2^-11 rms =
+0.43 eps / 2 rms, are not passed by any of the 10^5 values checked (chance
+2e-9 each); in norm they add in squares, (2^-11 / sqrt(3))^2 against the
+(eps / 2)^2 allowed: under a hundredth.
 """
 import numpy as np
 import pytest
@@ -49,7 +59,7 @@ def make(act, xd, bd, resid, r, gk, kg, ke, T, d, f, bias=0.5, T_max=None, devic
     return w, layer, L.Layer(cfg, inputs, on_device=device), x_to_device(inputs["X"], xd)
 
 
-def check_y(Y, ref, xd):
+def check_y(Y, ref, xd, one_part=False):
     y = y_to_host(Y)
     assert np.isfinite(y).all()
     if xd == "f32":
@@ -59,6 +69,8 @@ def check_y(Y, ref, xd):
     e = np.linalg.norm(y - ref) / np.linalg.norm(ref)
     assert e <= 1.05 * STEP[xd], e
     bar = STEP[xd] * (np.abs(ref) + 0.05 * np.abs(ref).max())
+    if one_part:
+        bar += 6 / np.sqrt(3) * 2.0 ** -11 * np.sqrt((ref ** 2).mean(axis=1, keepdims=True))
     assert (np.abs(y - ref) <= bar).all(), float((np.abs(y - ref) / bar).max())
     return e
 
@@ -112,14 +124,15 @@ def test_matches_oracle(case):
         lay.forward_few(X, Y, route_bufs=bufs)
         torch.cuda.synchronize()
         check_routing(route_to_host(bufs), rt, w, w.T)
-        e = check_y(Y, ref, w.x_dtype)
+        one = case[1] == "bf16" and case[2] != "bf16"
+        e = check_y(Y, ref, w.x_dtype, one)
         say(f"[few] err {e:.2e}")
         # without routing outputs, and again: the same bits
         raw = torch.int32 if w.x_dtype == "f32" else torch.int16
         assert torch.equal(lay.forward_few(X).view(raw), Y.view(raw))
         # fewer tokens after more: nothing of the earlier pass is read
         for T in {1, w.T // 2} - {0, w.T}:
-            check_y(lay.forward_few(X[:T].contiguous()), ref[:T], w.x_dtype)
+            check_y(lay.forward_few(X[:T].contiguous()), ref[:T], w.x_dtype, one)
         assert torch.equal(lay.forward_few(X).view(raw), Y.view(raw))
     finally:
         lay.close()
@@ -139,7 +152,7 @@ def test_workload_layers(wi, T):
         Y = lay.forward_few(X, route_bufs=bufs)
         torch.cuda.synchronize()
         check_routing(route_to_host(bufs), rt, w, T)
-        e = check_y(Y, O.forward(layer, routing=rt), w.x_dtype)
+        e = check_y(Y, O.forward(layer, routing=rt), w.x_dtype, w.x_dtype == "bf16" and w.base_dtype != "bf16")
         say(f"[few] {w.name} T={T}: err {e:.2e}")
         # passes of both kinds on one handle do not disturb each other
         Yf = lay.forward(X)
@@ -290,7 +303,7 @@ def test_a_four_bit_base_runs_nowhere_else():
         r = route_to_host(lay.route(many))
         rt = O.route(layer)
         assert np.array_equal(r["idx"], np.tile(rt["idx"], (8, 1)))
-        check_y(lay.forward_few(X), O.forward(layer), "bf16")
+        check_y(lay.forward_few(X), O.forward(layer), "bf16", True)
     finally:
         lay.close()
 
