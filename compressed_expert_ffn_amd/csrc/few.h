@@ -61,15 +61,12 @@ struct FewArgs {
   int zero_row;   // row of H that stays zero (the last of the workspace)
 };
 
-// Columns of f per input-projection workgroup (32 weight columns).
-inline __host__ __device__ int few_fcols(int Pin) { return 32 / Pin; }
 // k splits of the score product over workgroups.
 int few_router_splits(int d, int NCp);
 // Whether the partials of h A_down are summed by a launch of their own.
 bool few_v_sum(const FewArgs& a);
-hipError_t launch_few_route(int xt, int ty, const FewArgs& a, hipStream_t st);
-hipError_t launch_few_up(int xt, int ty, bool q4, const FewArgs& a, hipStream_t st);
-hipError_t launch_few_down(int xt, int ty, bool q4, const FewArgs& a, hipStream_t st);
+// The pass: activations xt, MFMAs ty, 4-bit base or not.
+hipError_t launch_few(int xt, int ty, bool q4, const FewArgs& a, hipStream_t st);
 
 // Base weights [rows n_in][cols] per group in device memory to the
 // fragment-major order of kernels.h; es: element bytes.  src1: the second of

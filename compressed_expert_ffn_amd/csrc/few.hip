@@ -79,37 +79,6 @@ __device__ __forceinline__ typename Frag<TY>::T raw_to_frag(const Raw<XT>& r) {
     return to_frag<TY>(v);
   }
 }
-template <int TY>
-__device__ __forceinline__ void frag_to_f32(const typename Frag<TY>::T& f, float (&o)[8]) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) o[e] = static_cast<float>(f[e]);
-}
-
-// Eight values of a residual factor as fp32: stored floats, or the codes of
-// one word with a scale each (s) or one scale (s1).
-template <int TY>
-__device__ __forceinline__ void factor8(int resid, const void* base, long i8, const uint16_t* s, bool one_scale,
-                                        float (&o)[8]) {
-  if (resid == RS_INT4) {
-    const uint32_t w = static_cast<const uint32_t*>(base)[i8];
-    if (one_scale) {
-      const float sc = f16_bits_to_f32(*s);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = int4_value(w, e, sc);
-    } else {
-      const u4v sv = *reinterpret_cast<const u4v*>(s);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t u = sv[e >> 1];
-        o[e] = int4_value(w, e, f16_bits_to_f32(static_cast<uint16_t>((u >> (16 * (e & 1))) & 0xFFFFu)));
-      }
-    }
-    return;
-  }
-  constexpr int es = TY == DT_F32 ? 4 : 2;
-  frag_to_f32<TY>(load_frag<TY>(static_cast<const char*>(base) + i8 * 8 * es), o);
-}
-
 // Type and 16-bit parts the gate-weighted hidden sums (and V) are held in for
 // the down product.  An fp16 number is exact to 2^-12, a sixteenth of what a
 // bf16 result is rounded by, so bf16 activations on fp16 MFMAs need one part;
@@ -142,12 +111,12 @@ __device__ __forceinline__ f4v mfma16k16(const uint16_t (&x)[4], const uint16_t 
     return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(p, r, c, 0, 0, 0);
 }
 // Its operand: four values (or the word holding four codes) of eight `at`, half `half`.
-template <int TY>
-__device__ __forceinline__ u4v load_down_factor(int resid, const void* Ad, long at, int half) {
+template <int TY, int RS>
+__device__ __forceinline__ u4v load_down_factor(const void* Ad, long at, int half) {
   u4v r = {0u, 0u, 0u, 0u};
   if constexpr (TY == DT_F32) {
     r = *reinterpret_cast<const u4v*>(static_cast<const float*>(Ad) + at * 8 + 4 * half);
-  } else if (resid == RS_INT4) {
+  } else if constexpr (RS == RS_INT4) {
     r[0] = static_cast<const uint32_t*>(Ad)[at] >> (16 * half);
   } else {
     const u2v d = *reinterpret_cast<const u2v*>(static_cast<const uint16_t*>(Ad) + at * 8 + 4 * half);
@@ -156,8 +125,8 @@ __device__ __forceinline__ u4v load_down_factor(int resid, const void* Ad, long 
   }
   return r;
 }
-template <int TY>
-__device__ __forceinline__ f4v down_factor(int resid, const u4v& ad, const float (&h)[4], f4v v) {
+template <int TY, int RS>
+__device__ __forceinline__ f4v down_factor(const u4v& ad, const float (&h)[4], f4v v) {
   if constexpr (TY == DT_F32) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
@@ -170,7 +139,7 @@ __device__ __forceinline__ f4v down_factor(int resid, const u4v& ad, const float
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t x = ad[0], y = ad[i >> 1];
-      w[i] = resid == RS_INT4 ? from_f32<TY>(static_cast<float>(static_cast<int>((x >> (4 * i)) & 15u) - 8))
+      w[i] = RS == RS_INT4 ? from_f32<TY>(static_cast<float>(static_cast<int>((x >> (4 * i)) & 15u) - 8))
                               : static_cast<uint16_t>((y >> (16 * (i & 1))) & 0xFFFFu);
       hi[i] = from_f32<TY>(h[i]);
       lo[i] = from_f32<TY>(h[i] - (TY == DT_F16 ? f16_bits_to_f32(hi[i]) : bf16_bits_to_f32(hi[i])));
@@ -651,7 +620,7 @@ __global__ __launch_bounds__(NT) void few_u_kernel(FewArgs a) {
 // grid: (touched group a) x (blocks of FT = 32 / Pin columns of f).  A
 // workgroup's 32 weight columns are 16 of the gate and the same 16 of the up
 // projection (SwiGLU), or 32 of the one input projection (GELU).
-template <int XT, int TY, bool Q4, int MT, int NWV>
+template <int XT, int TY, bool Q4, int RS, int MT, int NWV>
 __global__ __launch_bounds__(NWV * 64) void few_up_kernel(FewArgs a) {
   using XE = typename Elem<XT>::T;
   using B = typename Frag<TY>::T;
@@ -679,7 +648,7 @@ __global__ __launch_bounds__(NWV * 64) void few_up_kernel(FewArgs a) {
   struct Job {
     int slot;
     float wgt;
-    u4v b[2][TY == DT_F32 ? 2 : 1], s[2], ad[2];
+    u4v b[2][TY == DT_F32 ? 2 : 1], s[2], ad[2];  // 4-bit: words in elements 0
     u2v as;
   } job;
   int je = 0, jslot = -1;  // expert, and the slot of the lane's token
@@ -692,13 +661,13 @@ __global__ __launch_bounds__(NWV * 64) void few_up_kernel(FewArgs a) {
     J.slot = jslot;
     J.wgt = a.w[max(jslot, 0)];
     constexpr int es = TY == DT_F32 ? 4 : 2;
-    const bool int4r = a.resid == RS_INT4;
+    constexpr bool int4r = RS == RS_INT4;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int p = Pin == 2 ? x : 0, col0 = Pin == 2 ? f0 : f0 + 16 * x;  // 16 columns of projection p
       const long blk = static_cast<long>(je * Pin + p) * (a.f / 32) + (col0 >> 5);
       const long at = blk * 64 + 32 * (q & 1) + (col0 & 16) + l;
-      if (int4r) {
+      if constexpr (int4r) {
         J.b[x][0][0] = static_cast<const uint32_t*>(a.B1)[at];
         J.s[x] = *reinterpret_cast<const u4v*>(a.B1_s + blk * RPAD + 8 * (q & 1));
       } else {
@@ -708,15 +677,17 @@ __global__ __launch_bounds__(NWV * 64) void few_up_kernel(FewArgs a) {
       }
       const int c0 = Pin == 2 ? f0 : col0;
       const long ad = ((static_cast<long>(je) * (a.f / 32) + (c0 >> 5)) * 2 + ((c0 >> 4) & 1)) * 64 + l + 32 * (q & 1);
-      if (Pin == 1 || x == 0) J.ad[x] = load_down_factor<TY>(a.resid, a.Ad, ad, q >> 1);
+      if (Pin == 1 || x == 0) J.ad[x] = load_down_factor<TY, RS>(a.Ad, ad, q >> 1);
     }
-    if (int4r)
+    if constexpr (int4r)
       J.as = *reinterpret_cast<const u2v*>(a.Ad_s + (static_cast<long>(je) * (a.f / 32) + (f0 >> 5)) * RPAD + 4 * q);
   };
-  const int jobs = a.resid != RS_NONE ? ne * MT : 0;
-  if (wave < jobs) job_find(wave);
+  const int jobs = RS != RS_NONE ? ne * MT : 0;
+  if constexpr (RS != RS_NONE)
+    if (wave < jobs) job_find(wave);
   auto between = [&]() {
-    if (wave < jobs) job_load(job);
+    if constexpr (RS != RS_NONE)
+      if (wave < jobs) job_load(job);
   };
   const int n64 = a.d / 64;
   const int u0 = n64 * wave / NWV, u1 = n64 * (wave + 1) / NWV;
@@ -845,7 +816,7 @@ __global__ __launch_bounds__(NWV * 64) void few_up_kernel(FewArgs a) {
       }
     }
   };
-  if (a.resid == RS_NONE) {
+  if constexpr (RS == RS_NONE) {
     // the group's experts are its base: one activation, their gates summed
     for (int v = threadIdx.x; v < n * FT; v += NWV * 64) {
       const int c = v % FT, i = v / FT;
@@ -855,114 +826,114 @@ __global__ __launch_bounds__(NWV * 64) void few_up_kernel(FewArgs a) {
       const float h = a.act == ACT_SWIGLU ? silu_f(z[0][t][c]) * z[1][t][c] : gelu_tanh_f(z[c >> 4][t][c & 15]);
       store_hidden(row, c, wgt * h);
     }
-    return;
-  }
-  // The group's touched experts, one (expert, tile of tokens) at a time per
-  // wavefront, everything transposed: MFMA rows are the 16 columns of f, MFMA
-  // columns the tokens.  z + B u: depth 32 = the 16 rank columns twice, against
-  // the two 16-bit parts of u (4-bit B: codes, the scales in u).  The result's
-  // lane holds 4 columns of f of its token, which is the operand form of
-  // 16x16x16 MFMAs, so h goes into V = A_down^T h (16 rank columns by tokens)
-  // from the registers, again in two parts.
-  float hsum[MT][2][4];
+  } else {
+    // The group's touched experts, one (expert, tile of tokens) at a time per
+    // wavefront, everything transposed: MFMA rows are the 16 columns of f, MFMA
+    // columns the tokens.  z + B u: depth 32 = the 16 rank columns twice, against
+    // the two 16-bit parts of u (4-bit B: codes, the scales in u).  The result's
+    // lane holds 4 columns of f of its token, which is the operand form of
+    // 16x16x16 MFMAs, so h goes into V = A_down^T h (16 rank columns by tokens)
+    // from the registers, again in two parts.
+    float hsum[MT][2][4];
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
+      for (int x = 0; x < 2; ++x)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) hsum[m][x][r] = 0.f;
-  for (int j = wave; j < jobs; j += NWV) {
-    const int mt = j % MT, e = je, t = 16 * mt + l;
-    const Job J = job;
-    // u, then the next job's operands behind it
-    float u[2][8];
+        for (int r = 0; r < 4; ++r) hsum[m][x][r] = 0.f;
+    for (int j = wave; j < jobs; j += NWV) {
+      const int mt = j % MT, e = je, t = 16 * mt + l;
+      const Job J = job;
+      // u, then the next job's operands behind it
+      float u[2][8];
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const float* up =
-          a.U + (static_cast<long>(min(t, a.T - 1)) * a.E + e) * Pin * 16 + (Pin == 2 ? x : 0) * 16 + 8 * (q & 1);
-      const f4v u0 = *reinterpret_cast<const f4v*>(up), u1 = *reinterpret_cast<const f4v*>(up + 4);
+      for (int x = 0; x < 2; ++x) {
+        const float* up =
+            a.U + (static_cast<long>(min(t, a.T - 1)) * a.E + e) * Pin * 16 + (Pin == 2 ? x : 0) * 16 + 8 * (q & 1);
+        const f4v u0 = *reinterpret_cast<const f4v*>(up), u1 = *reinterpret_cast<const f4v*>(up + 4);
 #pragma unroll
-      for (int r = 0; r < 8; ++r) u[x][r] = r < 4 ? u0[r] : u1[r - 4];
-    }
-    if (j + NWV < jobs) {
-      job_find(j + NWV);
-      job_load(job);
-    }
-    if (!__any(J.slot >= 0)) continue;
-    const int part = q >> 1;
-    float hv[2][4];
+        for (int r = 0; r < 8; ++r) u[x][r] = r < 4 ? u0[r] : u1[r - 4];
+      }
+      if (j + NWV < jobs) {
+        job_find(j + NWV);
+        job_load(job);
+      }
+      if (!__any(J.slot >= 0)) continue;
+      const int part = q >> 1;
+      float hv[2][4];
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      B bw;
-      if constexpr (TY == DT_F32) {
-        Raw<DT_F32> r;
-        r.v[0] = J.b[x][0];
-        r.v[1] = J.b[x][1];
-        bw = raw_to_frag<DT_F32, DT_F32>(r);
-      } else if (a.resid == RS_INT4) {
-        const uint32_t word = J.b[x][0][0];
-        bw = int4_frag_1scale<TY>(word, 0x3C00);  // the codes themselves
+      for (int x = 0; x < 2; ++x) {
+        B bw;
+        if constexpr (TY == DT_F32) {
+          Raw<DT_F32> r;
+          r.v[0] = J.b[x][0];
+          r.v[1] = J.b[x][1];
+          bw = raw_to_frag<DT_F32, DT_F32>(r);
+        } else if constexpr (RS == RS_INT4) {
+          const uint32_t word = J.b[x][0][0];
+          bw = int4_frag_1scale<TY>(word, 0x3C00);  // the codes themselves
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          const uint32_t w = J.s[x][r >> 1];
-          u[x][r] *= f16_bits_to_f32(static_cast<uint16_t>((w >> (16 * (r & 1))) & 0xFFFFu));
+          for (int r = 0; r < 8; ++r) {
+            const uint32_t w = J.s[x][r >> 1];
+            u[x][r] *= f16_bits_to_f32(static_cast<uint16_t>((w >> (16 * (r & 1))) & 0xFFFFu));
+          }
+        } else {
+          bw = __builtin_bit_cast(B, J.b[x][0]);
         }
-      } else {
-        bw = __builtin_bit_cast(B, J.b[x][0]);
+        B bu = to_frag<TY>(u[x]);
+        if constexpr (TY == DT_F32) {
+          if (part) bu = zero_frag<TY>();
+        } else {
+          float rest[8];
+#pragma unroll
+          for (int r = 0; r < 8; ++r) rest[r] = u[x][r] - static_cast<float>(bu[r]);
+          const u4v hi = __builtin_bit_cast(u4v, bu), lo = __builtin_bit_cast(u4v, to_frag<TY>(rest));
+          bu = __builtin_bit_cast(B, part ? lo : hi);
+        }
+        const f4v zz = mfma16<TY>(bw, bu, *reinterpret_cast<const f4v*>(&z[x][t][4 * q]));
+#pragma unroll
+        for (int r = 0; r < 4; ++r) hv[x][r] = zz[r];
       }
-      B bu = to_frag<TY>(u[x]);
-      if constexpr (TY == DT_F32) {
-        if (part) bu = zero_frag<TY>();
-      } else {
-        float rest[8];
+      // a token without the expert keeps nothing of what its lane computed
+      f4v v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int r = 0; r < 8; ++r) rest[r] = u[x][r] - static_cast<float>(bu[r]);
-        const u4v hi = __builtin_bit_cast(u4v, bu), lo = __builtin_bit_cast(u4v, to_frag<TY>(rest));
-        bu = __builtin_bit_cast(B, part ? lo : hi);
+      for (int x = 0; x < 2; ++x) {
+        if (Pin == 2 && x == 1) break;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float h = Pin == 2 ? silu_f(hv[0][r]) * hv[1][r] : gelu_tanh_f(hv[x][r]);
+          hv[x][r] = J.slot >= 0 ? J.wgt * h : 0.f;
+#pragma unroll
+          for (int m = 0; m < MT; ++m) hsum[m][x][r] += m == mt ? hv[x][r] : 0.f;
+        }
+        v = down_factor<TY, RS>(J.ad[x], hv[x], v);
       }
-      const f4v zz = mfma16<TY>(bw, bu, *reinterpret_cast<const f4v*>(&z[x][t][4 * q]));
+      if constexpr (RS == RS_INT4) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) hv[x][r] = zz[r];
-    }
-    // a token without the expert keeps nothing of what its lane computed
-    f4v v = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      if (Pin == 2 && x == 1) break;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float h = Pin == 2 ? silu_f(hv[0][r]) * hv[1][r] : gelu_tanh_f(hv[x][r]);
-        hv[x][r] = J.slot >= 0 ? J.wgt * h : 0.f;
-#pragma unroll
-        for (int m = 0; m < MT; ++m) hsum[m][x][r] += m == mt ? hv[x][r] : 0.f;
+        for (int r = 0; r < 4; ++r) v[r] *= scale_at(J.as, r);
       }
-      v = down_factor<TY>(a.resid, J.ad[x], hv[x], v);
+      if (J.slot >= 0) *reinterpret_cast<f4v*>(a.Vp + (static_cast<long>(fb) * a.T * a.k + J.slot) * 16 + 4 * q) = v;
     }
-    if (a.resid == RS_INT4) {
+    // sum over the wavefronts' experts: [wave][m][16 tokens][FT columns]
 #pragma unroll
-      for (int r = 0; r < 4; ++r) v[r] *= scale_at(J.as, r);
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if (Pin == 2 && x == 1) break;
+        f4v o;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) o[r] = hsum[m][x][r];
+        *reinterpret_cast<f4v*>(red + ((wave * MT + m) * 16 + l) * FT + 16 * x + 4 * q) = o;
+      }
+    __syncthreads();
+    for (int v = threadIdx.x; v < n * FT; v += NWV * 64) {
+      const int c = v % FT, i = v / FT;
+      const int t = srow[i] >> 16, row = srow[i] & 0xFFFF;
+      float s = 0.f;
+      const int used = min(jobs, NWV);
+      for (int w = 0; w < used; ++w) s += red[((w * MT + (t >> 4)) * 16 + (t & 15)) * FT + c];
+      store_hidden(row, c, s);
     }
-    if (J.slot >= 0) *reinterpret_cast<f4v*>(a.Vp + (static_cast<long>(fb) * a.T * a.k + J.slot) * 16 + 4 * q) = v;
-  }
-  // sum over the wavefronts' experts: [wave][m][16 tokens][FT columns]
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      if (Pin == 2 && x == 1) break;
-      f4v o;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) o[r] = hsum[m][x][r];
-      *reinterpret_cast<f4v*>(red + ((wave * MT + m) * 16 + l) * FT + 16 * x + 4 * q) = o;
-    }
-  __syncthreads();
-  for (int v = threadIdx.x; v < n * FT; v += NWV * 64) {
-    const int c = v % FT, i = v / FT;
-    const int t = srow[i] >> 16, row = srow[i] & 0xFFFF;
-    float s = 0.f;
-    const int used = min(jobs, NWV);
-    for (int w = 0; w < used; ++w) s += red[((w * MT + (t >> 4)) * 16 + (t & 15)) * FT + c];
-    store_hidden(row, c, s);
   }
 }
 
@@ -1003,11 +974,11 @@ __global__ __launch_bounds__(NT) void few_vsum_kernel(FewArgs a) {
 // which then splits into two 16-bit parts like the hidden sums.
 constexpr int kDownPartials = 16;  // partials of V a thread holds in registers
 
-template <int XT, int TY, bool Q4, int MT>
+template <int XT, int TY, bool Q4, int RS, int MT>
 __global__ __launch_bounds__(NT) void few_down_kernel(FewArgs a) {
   using B = typename Frag<TY>::T;
   extern __shared__ __attribute__((aligned(16))) float red[];  // [NW][MT][256], V and a zero row, partials, grow
-  const int n = blockIdx.x, nv = a.resid != RS_NONE ? a.T * a.k * 16 : 0;
+  const int n = blockIdx.x, nv = RS != RS_NONE ? a.T * a.k * 16 : 0;
   float* V = red + NW * MT * 256;
   float* vpart = V + nv + 16;
   int16_t* grow = reinterpret_cast<int16_t*>(vpart + (nv && !a.v_sum ? NT : 0));
@@ -1085,7 +1056,7 @@ __global__ __launch_bounds__(NT) void few_down_kernel(FewArgs a) {
     // rank column 8 hh .. of expert j in the permuted depth order
     const int ks = 4 * (j >> 2) + 2 * (j & 1) + hh;
     const long at = (static_cast<long>(n32) * (a.NV / 16) + ks) * 64 + 16 * (n & 1) + l + 32 * ((j >> 1) & 1);
-    if (a.resid == RS_INT4) {
+    if constexpr (RS == RS_INT4) {
       T.w[0][0] = static_cast<const uint32_t*>(a.Bd)[g * a.bd_gs + at];
       T.s = *reinterpret_cast<const u4v*>(a.Bd_s + (static_cast<long>(e) * (a.d / 32) + n32) * RPAD + 8 * hh);
     } else {
@@ -1096,7 +1067,8 @@ __global__ __launch_bounds__(NT) void few_down_kernel(FewArgs a) {
 #pragma unroll
     for (int m = 0; m < TM; ++m) T.slot[m] = te_slot[m];
   };
-  if (wave < steps) tail_find(wave);
+  if constexpr (RS != RS_NONE)
+    if (wave < steps) tail_find(wave);
   auto tail_use = [&](const Tail& tail) {
     B b;
     if constexpr (TY == DT_F32) {
@@ -1104,7 +1076,7 @@ __global__ __launch_bounds__(NT) void few_down_kernel(FewArgs a) {
       r.v[0] = tail.w[0];
       r.v[1] = tail.w[1];
       b = raw_to_frag<DT_F32, DT_F32>(r);
-    } else if (a.resid == RS_INT4) {
+    } else if constexpr (RS == RS_INT4) {
       const uint32_t word = tail.w[0][0];
       b = int4_frag_1scale<TY>(word, 0x3C00);  // the codes themselves
     } else {
@@ -1117,7 +1089,7 @@ __global__ __launch_bounds__(NT) void few_down_kernel(FewArgs a) {
 #pragma unroll
       for (int r = 0; r < 8; ++r) {
         v[r] = vp[r];
-        if (TY != DT_F32 && a.resid == RS_INT4) {
+        if constexpr (RS == RS_INT4) {
           const uint32_t w = tail.s[r >> 1];
           v[r] *= f16_bits_to_f32(static_cast<uint16_t>((w >> (16 * (r & 1))) & 0xFFFFu));
         }
@@ -1142,7 +1114,7 @@ __global__ __launch_bounds__(NT) void few_down_kernel(FewArgs a) {
   // once the weights are under way: the first tail step, and V into LDS (from
   // the sum's launch, or summed here in an order set by T, k and f alone)
   auto between = [&]() {
-    if (!nv) return;
+    if constexpr (RS == RS_NONE) return;
     if (wave < steps) tail_load(tail);
     if (tid < 16) V[nv + tid] = 0.f;
     if (a.v_sum) {
@@ -1236,7 +1208,7 @@ __global__ __launch_bounds__(NT) void few_down_kernel(FewArgs a) {
         },
         between);
   }
-  if (nv) {
+  if constexpr (RS != RS_NONE) {
     __syncthreads();  // V is in LDS
     for (int i = wave; i < steps; i += NW) {
       const Tail now = tail;
@@ -1314,28 +1286,25 @@ hipError_t route_mt(const FewArgs& a, hipStream_t st) {
     if (e == hipSuccess && !a.u_all) e = go(few_u_kernel<XT, TY, RS, MT>, nub, NT, tiles, a, st);
   return e;
 }
-template <int XT, int TY, int RS>
-hipError_t route_rs(const FewArgs& a, hipStream_t st) {
-  return a.T <= 16 ? route_mt<XT, TY, RS, 1>(a, st) : route_mt<XT, TY, RS, 2>(a, st);
-}
-
-template <int XT, int TY, bool Q4, int MT>
+template <int XT, int TY, bool Q4, int RS, int MT>
 hipError_t up_mt(const FewArgs& a, hipStream_t st) {
   const unsigned grid = static_cast<unsigned>(a.G < a.T * a.kg ? a.G : a.T * a.kg) * (a.f * a.Pin / 32);
   const size_t lds = sizeof(float) * 2 * MT * 256;  // per wavefront
-  if (grid > 256) return go(few_up_kernel<XT, TY, Q4, MT, 8>, grid, 512, 8 * lds, a, st);
-  return go(few_up_kernel<XT, TY, Q4, MT, 16>, grid, 1024, 16 * lds, a, st);
-}
-template <int XT, int TY, bool Q4>
-hipError_t up_q(const FewArgs& a, hipStream_t st) {
-  return a.T <= 16 ? up_mt<XT, TY, Q4, 1>(a, st) : up_mt<XT, TY, Q4, 2>(a, st);
+  // More workgroups than compute units: smaller ones, so that one's expert
+  // steps overlap the others' streams and the last round is finer.  Without a
+  // residual there are no steps and 8 wavefronts keep the longer stream.
+  // Measured (us a pass, 4 / 8 / 16 wavefronts): INT4 layer T = 16 89 / 91 /
+  // 106, fp16 layer T = 5 33.0 / 34.2 / 41, flat layer T = 2 236 / 229 / 239.
+  constexpr int W = RS == RS_NONE ? 8 : 4;
+  if (grid > 256) return go(few_up_kernel<XT, TY, Q4, RS, MT, W>, grid, W * 64, W * lds, a, st);
+  return go(few_up_kernel<XT, TY, Q4, RS, MT, 16>, grid, 1024, 16 * lds, a, st);
 }
 
-template <int XT, int TY, bool Q4>
-hipError_t down_q(const FewArgs& a, hipStream_t st) {
+template <int XT, int TY, bool Q4, int RS>
+hipError_t down_rs(const FewArgs& a, hipStream_t st) {
   const unsigned grid = a.d / 16;
   const int groups = a.G < a.T * a.kg ? a.G : a.T * a.kg;
-  const int nv = a.resid != RS_NONE ? a.T * a.k * 16 : 0;
+  const int nv = RS != RS_NONE ? a.T * a.k * 16 : 0;
   if (nv && a.v_sum) {
     hipLaunchKernelGGL(few_vsum_kernel, dim3((nv + 63) / 64), dim3(NT), 0, st, a);
     const hipError_t e = hipGetLastError();
@@ -1345,10 +1314,18 @@ hipError_t down_q(const FewArgs& a, hipStream_t st) {
   const int mt = planes == 1 ? (a.T <= 16 ? 1 : 2) : a.T <= 8 ? 1 : a.T <= 16 ? 2 : 4;
   const size_t lds = sizeof(float) * (static_cast<size_t>(NW) * mt * 256 + nv + 16 + (nv && !a.v_sum ? NT : 0)) +
                      sizeof(int16_t) * groups * FEW_MAX_T;
-  if (mt == 1) return go(few_down_kernel<XT, TY, Q4, 1>, grid, NT, lds, a, st);
-  if (mt == 2) return go(few_down_kernel<XT, TY, Q4, 2>, grid, NT, lds, a, st);
-  if constexpr (planes == 2) return go(few_down_kernel<XT, TY, Q4, 4>, grid, NT, lds, a, st);
+  if (mt == 1) return go(few_down_kernel<XT, TY, Q4, RS, 1>, grid, NT, lds, a, st);
+  if (mt == 2) return go(few_down_kernel<XT, TY, Q4, RS, 2>, grid, NT, lds, a, st);
+  if constexpr (planes == 2) return go(few_down_kernel<XT, TY, Q4, RS, 4>, grid, NT, lds, a, st);
   return hipErrorInvalidValue;
+}
+
+template <int XT, int TY, bool Q4, int RS>
+hipError_t pass(const FewArgs& a, hipStream_t st) {
+  hipError_t e = a.T <= 16 ? route_mt<XT, TY, RS, 1>(a, st) : route_mt<XT, TY, RS, 2>(a, st);
+  if (e == hipSuccess) e = a.T <= 16 ? up_mt<XT, TY, Q4, RS, 1>(a, st) : up_mt<XT, TY, Q4, RS, 2>(a, st);
+  if (e == hipSuccess) e = down_rs<XT, hidden_type(TY, Q4), Q4, RS>(a, st);
+  return e;
 }
 
 }  // namespace
@@ -1369,44 +1346,23 @@ bool few_v_sum(const FewArgs& a) {
   return (nfb + parts - 1) / parts > kDownPartials;
 }
 
-hipError_t launch_few_route(int xt, int ty, const FewArgs& a, hipStream_t st) {
+hipError_t launch_few(int xt, int ty, bool q4, const FewArgs& a, hipStream_t st) {
   const int rs = a.resid == RS_NONE ? 0 : a.resid == RS_INT4 ? 2 : 1;
-  switch (xt * 16 + ty * 4 + rs) {
-    case 0: return route_rs<DT_F32, DT_F32, RS_NONE>(a, st);
-    case 1: return route_rs<DT_F32, DT_F32, RS_F32>(a, st);
-    case 16 + 4: return route_rs<DT_F16, DT_F16, RS_NONE>(a, st);
-    case 16 + 5: return route_rs<DT_F16, DT_F16, RS_F16>(a, st);
-    case 16 + 6: return route_rs<DT_F16, DT_F16, RS_INT4>(a, st);
-    case 32 + 8: return route_rs<DT_BF16, DT_BF16, RS_NONE>(a, st);
-    case 32 + 10: return route_rs<DT_BF16, DT_BF16, RS_INT4>(a, st);
-    case 32 + 4: return route_rs<DT_BF16, DT_F16, RS_NONE>(a, st);
-    case 32 + 5: return route_rs<DT_BF16, DT_F16, RS_F16>(a, st);
-    case 32 + 6: return route_rs<DT_BF16, DT_F16, RS_INT4>(a, st);
-  }
-  return hipErrorInvalidValue;
-}
-
-hipError_t launch_few_up(int xt, int ty, bool q4, const FewArgs& a, hipStream_t st) {
-  switch (xt * 8 + ty * 2 + (q4 ? 1 : 0)) {
-    case 0: return up_q<DT_F32, DT_F32, false>(a, st);
-    case 8 + 2: return up_q<DT_F16, DT_F16, false>(a, st);
-    case 8 + 3: return up_q<DT_F16, DT_F16, true>(a, st);
-    case 16 + 4: return up_q<DT_BF16, DT_BF16, false>(a, st);
-    case 16 + 5: return up_q<DT_BF16, DT_BF16, true>(a, st);
-    case 16 + 2: return up_q<DT_BF16, DT_F16, false>(a, st);
-  }
-  return hipErrorInvalidValue;
-}
-
-hipError_t launch_few_down(int xt, int ty, bool q4, const FewArgs& a, hipStream_t st) {
-  ty = hidden_type(ty, q4);
-  switch (xt * 8 + ty * 2 + (q4 ? 1 : 0)) {
-    case 0: return down_q<DT_F32, DT_F32, false>(a, st);
-    case 8 + 2: return down_q<DT_F16, DT_F16, false>(a, st);
-    case 8 + 3: return down_q<DT_F16, DT_F16, true>(a, st);
-    case 16 + 4: return down_q<DT_BF16, DT_BF16, false>(a, st);
-    case 16 + 3: return down_q<DT_BF16, DT_F16, true>(a, st);
-    case 16 + 2: return down_q<DT_BF16, DT_F16, false>(a, st);
+  switch (xt * 100 + ty * 10 + rs + (q4 ? 5 : 0)) {
+    case 0: return pass<DT_F32, DT_F32, false, RS_NONE>(a, st);
+    case 1: return pass<DT_F32, DT_F32, false, RS_F32>(a, st);
+    case 110: return pass<DT_F16, DT_F16, false, RS_NONE>(a, st);
+    case 111: return pass<DT_F16, DT_F16, false, RS_F16>(a, st);
+    case 112: return pass<DT_F16, DT_F16, false, RS_INT4>(a, st);
+    case 115: return pass<DT_F16, DT_F16, true, RS_NONE>(a, st);
+    case 117: return pass<DT_F16, DT_F16, true, RS_INT4>(a, st);
+    case 220: return pass<DT_BF16, DT_BF16, false, RS_NONE>(a, st);
+    case 222: return pass<DT_BF16, DT_BF16, false, RS_INT4>(a, st);
+    case 225: return pass<DT_BF16, DT_BF16, true, RS_NONE>(a, st);
+    case 227: return pass<DT_BF16, DT_BF16, true, RS_INT4>(a, st);
+    case 210: return pass<DT_BF16, DT_F16, false, RS_NONE>(a, st);
+    case 211: return pass<DT_BF16, DT_F16, false, RS_F16>(a, st);
+    case 212: return pass<DT_BF16, DT_F16, false, RS_INT4>(a, st);
   }
   return hipErrorInvalidValue;
 }

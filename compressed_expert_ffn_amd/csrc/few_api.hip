@@ -159,9 +159,7 @@ extern "C" int moe_forward_few(moe_handle* h, const void* X, int32_t T, void* Y,
   a.eslot = s.eslot;
   hipStream_t st = static_cast<hipStream_t>(stream);
   a.v_sum = few_v_sum(a) ? 1 : 0;
-  hipError_t e = launch_few_route(c.x_dtype, h->mma, a, st);
-  if (e == hipSuccess) e = launch_few_up(c.x_dtype, h->mma, q4, a, st);
-  if (e == hipSuccess) e = launch_few_down(c.x_dtype, h->mma, q4, a, st);
+  const hipError_t e = launch_few(c.x_dtype, h->mma, q4, a, st);
   if (e != hipSuccess) return fail(MOE_ERR_HIP, "few-token launch: %s", hipGetErrorString(e));
   return MOE_OK;
 }
