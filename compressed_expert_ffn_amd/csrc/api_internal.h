@@ -48,7 +48,7 @@ struct FewState {
   int *idx = nullptr, *gidx = nullptr, *glist = nullptr, *elist = nullptr, *ticket = nullptr;
   int4* grec = nullptr;
   int16_t *grow = nullptr, *eslot = nullptr;
-  float *w = nullptr, *L = nullptr, *U = nullptr, *Vp = nullptr, *V = nullptr;
+  float *w = nullptr, *bias = nullptr, *L = nullptr, *U = nullptr, *Vp = nullptr, *V = nullptr;
   void* H = nullptr;
 };
 

@@ -18,7 +18,8 @@ struct FewArgs {
   // router (layout in kernels.h)
   const float* Wr;
   int NCp, nsplit;
-  const float *gbias, *ebias;
+  const float* bias;  // [score columns]: group then expert biases
+  uint32_t over_nc, over_kg, over_ke, over_k;  // ceil(2^32 / n) of the score columns, kg, ke and k (0 for n = 1)
   float* L;       // [nsplit][T][NCp] partial scores
   int* ticket;    // zero between passes
   // routing results, and the caller's lists (null where not asked for)
@@ -62,7 +63,7 @@ struct FewArgs {
 };
 
 // k splits of the score product over workgroups.
-int few_router_splits(int d, int NCp);
+int few_router_splits(int d);
 // Whether the partials of h A_down are summed by a launch of their own.
 bool few_v_sum(const FewArgs& a);
 // The pass: activations xt, MFMAs ty, 4-bit base or not.

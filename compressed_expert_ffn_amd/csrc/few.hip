@@ -79,6 +79,24 @@ __device__ __forceinline__ typename Frag<TY>::T raw_to_frag(const Raw<XT>& r) {
     return to_frag<TY>(v);
   }
 }
+// fp32 to a 16-bit MFMA type by the hardware's conversions (nearest, ties to even).
+template <int TY>
+__device__ __forceinline__ typename Frag<TY>::T round_frag(const float (&v)[8]) {
+  typename Frag<TY>::T r;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (TY == DT_BF16) r[i] = static_cast<__bf16>(v[i]);
+    else if constexpr (TY == DT_F16) r[i] = static_cast<_Float16>(v[i]);
+    else r[i] = v[i];
+  }
+  return r;
+}
+template <int TY>
+__device__ __forceinline__ uint16_t round_bits(float v) {
+  if constexpr (TY == DT_BF16) return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
+  else return f32_to_f16_bits(v);
+}
+
 // Type and 16-bit parts the gate-weighted hidden sums (and V) are held in for
 // the down product.  An fp16 number is exact to 2^-12, a sixteenth of what a
 // bf16 result is rounded by, so bf16 activations on fp16 MFMAs need one part;
@@ -139,10 +157,10 @@ __device__ __forceinline__ f4v down_factor(const u4v& ad, const float (&h)[4], f
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t x = ad[0], y = ad[i >> 1];
-      w[i] = RS == RS_INT4 ? from_f32<TY>(static_cast<float>(static_cast<int>((x >> (4 * i)) & 15u) - 8))
+      w[i] = RS == RS_INT4 ? round_bits<TY>(static_cast<float>(static_cast<int>((x >> (4 * i)) & 15u) - 8))
                               : static_cast<uint16_t>((y >> (16 * (i & 1))) & 0xFFFFu);
-      hi[i] = from_f32<TY>(h[i]);
-      lo[i] = from_f32<TY>(h[i] - (TY == DT_F16 ? f16_bits_to_f32(hi[i]) : bf16_bits_to_f32(hi[i])));
+      hi[i] = round_bits<TY>(h[i]);
+      lo[i] = round_bits<TY>(h[i] - (TY == DT_F16 ? f16_bits_to_f32(hi[i]) : bf16_bits_to_f32(hi[i])));
     }
     return mfma16k16<TY>(w, lo, mfma16k16<TY>(w, hi, v));
   }
@@ -350,51 +368,33 @@ __device__ void u_block(const FewArgs& a, int g, int nb, float* red) {
 struct SelectLds {
   int idx[FEW_MAX_T * MAX_SLOTS], gid[FEW_MAX_T * MAX_KG];
   float pg[FEW_MAX_T * MAX_KG];
-  int gcount[256], ecount[1024], gpos[256], epos[1024];
-  int wsum[NW];
+  int count[2][1024], pos[2][1024];  // tokens per group and per expert; non-empty bins before each
+  int wsum[2][NW];
   int last;
 };
 
-// Number of non-zero counts before each id (a non-zero one's position among
-// them), by all threads for up to NT counts; returns how many there are.
-__device__ int compact(const int* count, int n, int* pos, int* wsum) {
-  const int tid = threadIdx.x, wave = wave_id(), lane = tid & 63;
-  const bool on = tid < n && count[tid] > 0;
-  const unsigned long long m = __ballot(on);
-  if (lane == 0) wsum[wave] = __popcll(m);
-  __syncthreads();
-  int before = 0, total = 0;
-#pragma unroll
-  for (int w = 0; w < NW; ++w) {
-    const int c = wsum[w];
-    before += w < wave ? c : 0;
-    total += c;
-  }
-  if (tid < n) pos[tid] = before + __popcll(m & ((1ull << lane) - 1));
-  __syncthreads();
-  return total;
+// i / n for i n < 2^32, over = ceil(2^32 / n), or 0 for n = 1.
+__device__ __forceinline__ int div_small(int i, uint32_t over) {
+  return over ? static_cast<int>(__umulhi(static_cast<uint32_t>(i), over)) : i;
 }
 
 // Scores of tokens t0 .. t0 + nt - 1 into sc [nt][NC], biases included: the
 // parts other workgroups stored, several elements' loads in flight at once.
-__device__ void gather_scores(const FewArgs& a, int t0, int nt, int NC, float* sc) {
+__device__ __forceinline__ void gather_scores(const FewArgs& a, int t0, int nt, int NC, float* sc) {
   const long stride = static_cast<long>(a.T) * a.NCp;
   const int total = nt * NC;
+#pragma unroll 1
   for (int e0 = threadIdx.x; e0 < total; e0 += 4 * NT) {
     float part[4][4], bias[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int e = e0 + j * NT;
-      const bool ok = e < total;
-      const int tk = ok ? e / NC : 0, c = ok ? e - tk * NC : 0;
+      const int e = min(e0 + j * NT, total - 1);
+      const int tk = div_small(e, a.over_nc), c = e - tk * NC;
       const float* p = a.L + static_cast<long>(t0 + tk) * a.NCp + c;
 #pragma unroll
       for (int s = 0; s < 4; ++s)
-        part[j][s] = ok && s < a.nsplit
-                         ? __hip_atomic_load(p + s * stride, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)
-                         : 0.f;
-      const float* bp = c < a.G ? a.gbias + c : a.ebias + (c - a.G);
-      bias[j] = ok && (c < a.G ? a.gbias != nullptr : a.ebias != nullptr) ? *bp : 0.f;
+        part[j][s] = s < a.nsplit ? __hip_atomic_load(p + s * stride, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0.f;
+      bias[j] = a.bias[c];
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -402,128 +402,145 @@ __device__ void gather_scores(const FewArgs& a, int t0, int nt, int NC, float* s
   }
 }
 
-// Selection for tokens t0 .. t0 + nt - 1 by one workgroup: larger score first,
-// ties to the lower index; gates are the softmax over the chosen groups times
-// the softmax over the chosen experts of each.
-__device__ void select_tokens(const FewArgs& a, int t0, int nt, int NC, const float* sc, SelectLds& s) {
+// Selection for tokens t0 .. t0 + nt - 1 by one workgroup, a wavefront per
+// token for the groups and then per (token, chosen group) for the experts:
+// larger score first, ties to the lower index; gates are the softmax over the
+// chosen groups times the softmax over the chosen experts of each.
+__device__ __forceinline__ void select_tokens(const FewArgs& a, int t0, int nt, int NC, const float* sc, SelectLds& s) {
   const int wave = wave_id(), lane = threadIdx.x & 63;
-  for (int i = wave; i < nt; i += NW) {
-    const int t = t0 + i;
-    float v;
-    int g;
-    wave_topk(sc + i * NC, a.G, a.kg, lane, v, g);
-    const float e = lane < a.kg ? expf(v - lane_value(v, 0)) : 0.f;
-    float sum = 0.f;
-    for (int r = 0; r < a.kg; ++r) sum += lane_value(e, r);
-    if (lane < a.kg) {
-      s.gid[t * a.kg + lane] = g;
-      s.pg[t * a.kg + lane] = e / sum;
-      a.gidx[t * a.kg + lane] = g;
-      if (a.K == 1) {
-        s.idx[t * a.k + lane] = g;
-        a.idx[t * a.k + lane] = g;
-        a.w[t * a.k + lane] = e / sum;
+#pragma unroll 1
+  for (int level = 0; level < (a.K > 1 ? 2 : 1); ++level) {
+    const int n = level ? a.K : a.G, k = level ? a.ke : a.kg, jobs = level ? nt * a.kg : nt;
+#pragma unroll 1
+    for (int i = wave; i < jobs; i += NW) {
+      const int tok = level ? div_small(i, a.over_kg) : i;
+      const int tr = t0 * a.kg + i;  // level 1: token * kg + rank
+      const float* from = sc + tok * NC + (level ? a.G + s.gid[tr] * a.K : 0);
+      float v;
+      int j;
+      wave_topk(from, n, k, lane, v, j);
+      const float e = lane < k ? expf(v - lane_value(v, 0)) : 0.f;
+      float sum = 0.f;
+#pragma unroll 1
+      for (int r = 0; r < k; ++r) sum += lane_value(e, r);
+      const float p = e / sum;
+      if (lane >= k) continue;
+      int at, id = j;
+      float w = p;
+      if (level) {
+        at = tr * a.ke + lane;  // (t * kg + rank) * ke + b
+        id += s.gid[tr] * a.K;
+        w *= s.pg[tr];
+      } else {
+        at = (t0 + i) * a.kg + lane;
+        s.gid[at] = j;
+        s.pg[at] = p;
+        a.gidx[at] = j;
+      }
+      if (level || a.K == 1) {
+        s.idx[at] = id;
+        a.idx[at] = id;
+        a.w[at] = w;
       }
     }
+    __syncthreads();
   }
-  __syncthreads();
-  if (a.K == 1) return;
-  for (int i = wave; i < nt * a.kg; i += NW) {
-    const int tr = t0 * a.kg + i, g = s.gid[tr];
-    float v;
-    int j;
-    wave_topk(sc + (i / a.kg) * NC + a.G + g * a.K, a.K, a.ke, lane, v, j);
-    const float e = lane < a.ke ? expf(v - lane_value(v, 0)) : 0.f;
-    float sum = 0.f;
-    for (int r = 0; r < a.ke; ++r) sum += lane_value(e, r);
-    if (lane < a.ke) {
-      const int slot = tr * a.ke + lane;  // (t * kg + rank) * ke + b
-      s.idx[slot] = g * a.K + j;
-      a.idx[slot] = g * a.K + j;
-      a.w[slot] = s.pg[tr] * (e / sum);
-    }
-  }
-  __syncthreads();
 }
 
-// The touched groups and experts with their tokens, and the caller's lists.
-// tab: room for (G + min(E, T*k)) * FEW_MAX_T int16.
-__device__ void make_lists(const FewArgs& a, SelectLds& s, int16_t* tab) {
+// The caller's lists: an entry's place in its bin's list is the entries of
+// lower bins and those before it in its own (tokens ascend within a bin).
+__device__ __noinline__ void caller_lists(const int* bins, int n, int nbins, int per, int* counts, int* offsets,
+                                          int* perm) {
   const int tid = threadIdx.x;
+#pragma unroll 1
+  for (int b = tid; b <= nbins; b += NT) {
+    int below = 0, mine = 0;
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      below += bins[i] < b ? 1 : 0;
+      mine += bins[i] == b ? 1 : 0;
+    }
+    if (counts && b < nbins) counts[b] = mine;
+    if (offsets) offsets[b] = below;
+  }
+  if (perm && tid < n) {
+    int at = 0;
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) at += (bins[i] < bins[tid] || (bins[i] == bins[tid] && i < tid)) ? 1 : 0;
+    perm[at] = tid / per;
+  }
+}
+
+// The touched groups and experts with their tokens.
+// tab: room for (G + min(E, T*k)) * FEW_MAX_T int16.
+__device__ __forceinline__ void make_lists(const FewArgs& a, SelectLds& s, int16_t* tab) {
+  const int tid = threadIdx.x, wave = wave_id(), lane = tid & 63;
   const int ng = a.T * a.kg, na = a.T * a.k;
   const bool resid = a.resid != RS_NONE;
-  // one token: its groups and experts are distinct and in place already
-  const bool one = a.T == 1;
-  if (one) {
-    if (tid == 0) a.glist[0] = ng;
+  if (a.T == 1) {
+    // its groups and experts are distinct and in place already
+    if (tid == 0) {
+      a.glist[0] = ng;
+      a.elist[0] = na;
+    }
     if (tid < ng) {
       a.grec[tid] = int4{s.gid[tid], tid * a.ke, a.ke, 1};
       a.grow[tid * FEW_MAX_T] = static_cast<int16_t>(tid);
     }
-    if (resid) {
-      if (tid == 0) a.elist[0] = na;
-      if (tid < na) {
-        a.elist[1 + tid] = s.idx[tid];
-        a.eslot[tid * FEW_MAX_T] = static_cast<int16_t>(tid);
-      }
+    if (resid && tid < na) {
+      a.elist[1 + tid] = s.idx[tid];
+      a.eslot[tid * FEW_MAX_T] = static_cast<int16_t>(tid);
     }
-    if (!a.wants_lists) return;
+    return;
   }
-  if (tid < a.G) s.gcount[tid] = 0;
-  if (tid < a.E) s.ecount[tid] = 0;
+  // groups and experts side by side: tokens per bin, non-empty bins before each
+  s.count[0][tid] = 0;
+  s.count[1][tid] = 0;
   __syncthreads();
-  if (tid < ng) atomicAdd(&s.gcount[s.gid[tid]], 1);
-  if (tid < na) atomicAdd(&s.ecount[s.idx[tid]], 1);
+  if (tid < ng) atomicAdd(&s.count[0][s.gid[tid]], 1);
+  if (tid < na) atomicAdd(&s.count[1][s.idx[tid]], 1);
   __syncthreads();
-  if (!one) {
-    const int tg = compact(s.gcount, a.G, s.gpos, s.wsum);
-    const int te = resid ? compact(s.ecount, a.E, s.epos, s.wsum) : 0;
-    int16_t* etab = tab + a.G * FEW_MAX_T;
-    for (int i = tid; i < tg * (FEW_MAX_T / 2); i += NT) reinterpret_cast<int*>(tab)[i] = -1;
-    for (int i = tid; i < te * (FEW_MAX_T / 2); i += NT) reinterpret_cast<int*>(etab)[i] = -1;
-    if (tid == 0) a.glist[0] = tg;
-    if (tid < a.G && s.gcount[tid] > 0) {
-      const int first = resid ? s.epos[tid * a.K] : 0, end = !resid ? 0 : tid + 1 < a.G ? s.epos[(tid + 1) * a.K] : te;
-      a.grec[s.gpos[tid]] = int4{tid, first, end - first, s.gcount[tid]};
-    }
-    if (resid) {
-      if (tid == 0) a.elist[0] = te;
-      if (tid < a.E && s.ecount[tid] > 0) a.elist[1 + s.epos[tid]] = tid;
-    }
-    __syncthreads();
-    if (tid < ng) tab[s.gpos[s.gid[tid]] * FEW_MAX_T + tid / a.kg] = static_cast<int16_t>(tid);
-    if (te && tid < na) etab[s.epos[s.idx[tid]] * FEW_MAX_T + tid / a.k] = static_cast<int16_t>(tid);
-    __syncthreads();
-    for (int i = tid; i < tg * (FEW_MAX_T / 2); i += NT)
-      reinterpret_cast<int*>(a.grow)[i] = reinterpret_cast<const int*>(tab)[i];
-    for (int i = tid; i < te * (FEW_MAX_T / 2); i += NT)
-      reinterpret_cast<int*>(a.eslot)[i] = reinterpret_cast<const int*>(etab)[i];
+  const unsigned long long m0 = __ballot(s.count[0][tid] > 0), m1 = __ballot(s.count[1][tid] > 0);
+  if (lane == 0) {
+    s.wsum[0][wave] = __popcll(m0);
+    s.wsum[1][wave] = __popcll(m1);
   }
-  if (!a.wants_lists) return;
-  // the caller's lists: an entry's place in its bin's list is the entries of
-  // lower bins and those before it in its own (tokens ascend within a bin)
-  if (a.gcounts && tid < a.G) a.gcounts[tid] = s.gcount[tid];
-  if (a.counts && tid < a.E) a.counts[tid] = s.ecount[tid];
-  if (a.goffsets && tid <= a.G) {
-    int n = 0;
-    for (int i = 0; i < ng; ++i) n += s.gid[i] < tid ? 1 : 0;
-    a.goffsets[tid] = n;
+  __syncthreads();
+  int before0 = 0, before1 = 0, tg = 0, te = 0;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    const int c0 = s.wsum[0][w], c1 = s.wsum[1][w];
+    before0 += w < wave ? c0 : 0;
+    before1 += w < wave ? c1 : 0;
+    tg += c0;
+    te += c1;
   }
-  if (a.offsets)
-    for (int e = tid; e <= a.E; e += NT) {
-      int n = 0;
-      for (int i = 0; i < na; ++i) n += s.idx[i] < e ? 1 : 0;
-      a.offsets[e] = n;
-    }
-  if (a.gperm && tid < ng) {
-    int at = 0;
-    for (int i = 0; i < ng; ++i) at += (s.gid[i] < s.gid[tid] || (s.gid[i] == s.gid[tid] && i < tid)) ? 1 : 0;
-    a.gperm[at] = tid / a.kg;
+  if (!resid) te = 0;
+  s.pos[0][tid] = before0 + __popcll(m0 & ((1ull << lane) - 1));
+  s.pos[1][tid] = before1 + __popcll(m1 & ((1ull << lane) - 1));
+  if (tid == 0) {
+    a.glist[0] = tg;
+    a.elist[0] = te;
   }
-  if (a.perm && tid < na) {
-    int at = 0;
-    for (int i = 0; i < na; ++i) at += (s.idx[i] < s.idx[tid] || (s.idx[i] == s.idx[tid] && i < tid)) ? 1 : 0;
-    a.perm[at] = tid / a.k;
+  // tables of the tokens in each, empty at first
+  int16_t* etab = tab + a.G * FEW_MAX_T;
+  for (int i = tid; i < tg * (FEW_MAX_T / 2); i += NT) reinterpret_cast<int*>(tab)[i] = -1;
+  for (int i = tid; i < te * (FEW_MAX_T / 2); i += NT) reinterpret_cast<int*>(etab)[i] = -1;
+  __syncthreads();
+  if (tid < ng) tab[s.pos[0][s.gid[tid]] * FEW_MAX_T + div_small(tid, a.over_kg)] = static_cast<int16_t>(tid);
+  if (resid && tid < na)
+    etab[s.pos[1][s.idx[tid]] * FEW_MAX_T + div_small(tid, a.over_k)] = static_cast<int16_t>(tid);
+  __syncthreads();
+  for (int i = tid; i < tg * (FEW_MAX_T / 2); i += NT)
+    reinterpret_cast<int*>(a.grow)[i] = reinterpret_cast<const int*>(tab)[i];
+  for (int i = tid; i < te * (FEW_MAX_T / 2); i += NT)
+    reinterpret_cast<int*>(a.eslot)[i] = reinterpret_cast<const int*>(etab)[i];
+  if (resid && s.count[1][tid] > 0) a.elist[1 + s.pos[1][tid]] = tid;
+  if (tid < a.G && s.count[0][tid] > 0) {
+    // an expert past the last has all touched ones before it
+    const int first = resid ? s.pos[1][tid * a.K] : 0;
+    const int end = !resid ? 0 : (tid + 1) * a.K < 1024 ? s.pos[1][(tid + 1) * a.K] : te;
+    a.grec[s.pos[0][tid]] = int4{tid, first, end - first, s.count[0][tid]};
   }
 }
 
@@ -552,29 +569,23 @@ __global__ __launch_bounds__(NT) void few_route_kernel(FewArgs a) {
   const int cb = blockIdx.x % ncb, split = blockIdx.x / ncb;
   score_block<XT, MT>(a, cb, split, red);
   __syncthreads();
-  if (nsb == 1) {
-    // up to 16 columns in all: this workgroup holds every score
-    for (int v = threadIdx.x; v < a.T * 16; v += NT) {
-      const int row = v >> 4, col = v & 15;
-      if (col >= NC) continue;
-      const float* bp = col < a.G ? a.gbias : a.ebias;
-      const float bias = bp ? bp[col < a.G ? col : col - a.G] : 0.f;
-      sc[row * NC + col] = block_sum<NW, 1, MT>(red, row, col) + bias;
-    }
-    __syncthreads();
-    select_tokens(a, 0, a.T, NC, sc, s);
-  } else {
-    // Scores go to memory past the caches (agent scope), each wavefront waits
-    // for its own stores, and the workgroup that counts itself in last selects;
-    // nobody waits for another.  The scores are read back past the caches too,
-    // so no cache needs writing back or dropping: a release fence here, which
-    // writes back the whole second-level cache, took 13 us of a 256-expert
-    // layer's launch.
-    for (int v = threadIdx.x; v < a.T * 16; v += NT) {
-      const int row = v >> 4, col = v & 15;
-      __hip_atomic_store(a.L + (static_cast<long>(split) * a.T + row) * a.NCp + cb * 16 + col,
-                         block_sum<NW, 1, MT>(red, row, col), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
+  const bool alone = nsb == 1;  // up to 16 columns in all: this workgroup holds every score
+  // Otherwise scores go to memory past the caches (agent scope), each wavefront
+  // waits for its own stores, and the workgroup that counts itself in last
+  // selects; nobody waits for another.  The scores are read back past the
+  // caches too, so no cache needs writing back or dropping: a release fence
+  // here, which writes back the whole second-level cache, took 13 us of a
+  // 256-expert layer's launch.
+  for (int v = threadIdx.x; v < a.T * 16; v += NT) {
+    const int row = v >> 4, col = v & 15;
+    const float sum = block_sum<NW, 1, MT>(red, row, col);
+    if (!alone)
+      __hip_atomic_store(a.L + (static_cast<long>(split) * a.T + row) * a.NCp + cb * 16 + col, sum, __ATOMIC_RELAXED,
+                         __HIP_MEMORY_SCOPE_AGENT);
+    else if (col < NC)
+      sc[row * NC + col] = sum + a.bias[col];
+  }
+  if (!alone) {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -585,15 +596,20 @@ __global__ __launch_bounds__(NT) void few_route_kernel(FewArgs a) {
     __syncthreads();
     if (!s.last) return;
     asm volatile("" ::: "memory");
-    const int chunk = select_chunk(a.T, NC);
-    for (int t0 = 0; t0 < a.T; t0 += chunk) {
-      const int nt = min(chunk, a.T - t0);
-      gather_scores(a, t0, nt, NC, sc);
-      __syncthreads();
-      select_tokens(a, t0, nt, NC, sc, s);
-    }
+  }
+  const int chunk = alone ? a.T : select_chunk(a.T, NC);
+#pragma unroll 1
+  for (int t0 = 0; t0 < a.T; t0 += chunk) {
+    const int nt = min(chunk, a.T - t0);
+    if (!alone) gather_scores(a, t0, nt, NC, sc);
+    __syncthreads();
+    select_tokens(a, t0, nt, NC, sc, s);
   }
   make_lists(a, s, reinterpret_cast<int16_t*>(red));
+  if (a.wants_lists) {
+    caller_lists(s.gid, a.T * a.kg, a.G, a.kg, a.gcounts, a.goffsets, a.gperm);
+    caller_lists(s.idx, a.T * a.k, a.E, a.k, a.counts, a.offsets, a.perm);
+  }
 }
 
 // U of the chosen experts only: one workgroup per 32 factor columns, idle
@@ -625,7 +641,7 @@ __global__ __launch_bounds__(NWV * 64) void few_up_kernel(FewArgs a) {
   using XE = typename Elem<XT>::T;
   using B = typename Frag<TY>::T;
   constexpr int HT = hidden_type(TY, Q4);
-  extern __shared__ __attribute__((aligned(16))) float red[];  // partial tiles, then the wavefronts' hidden sums
+  extern __shared__ __attribute__((aligned(16))) float red[];  // partial tiles, then the weighted h
   __shared__ __attribute__((aligned(16))) float z[2][MT * 16][20];  // 20: rows 16 bytes apart mod 128
   __shared__ int srow[FEW_MAX_T];   // (token << 16) | row t*kg + rank, of the group's tokens
   const int Pin = a.Pin, FT = 32 / Pin, nfb = a.f / FT;
@@ -635,14 +651,13 @@ __global__ __launch_bounds__(NWV * 64) void few_up_kernel(FewArgs a) {
   const int g = rec.x, first = rec.y, ne = rec.z, n = rec.w;
   const int wave = wave_id(), lane = threadIdx.x & 63, l = lane & 15, q = lane >> 4;
   const int f0 = fb * FT;
-  // the group's tokens
-  if (wave == 0) {
-    const int row = lane < a.T ? a.grow[ga * FEW_MAX_T + lane] : -1;
-    const unsigned long long m = __ballot(row >= 0);
-    if (row >= 0) srow[__popcll(m & ((1ull << lane) - 1))] = (lane << 16) | row;
-  }
-  // The wavefront's jobs: (touched expert, tile of 16 tokens), expert first +
-  // wave, + NWV, ...  Their operands are few but cold, and behind a stream
+  // the group's tokens (bit t), their rows
+  const int grow = lane < a.T ? a.grow[ga * FEW_MAX_T + lane] : -1;
+  const uint32_t members = static_cast<uint32_t>(__ballot(grow >= 0));
+  if (wave == 0 && grow >= 0) srow[__popc(members & ((1u << lane) - 1))] = (lane << 16) | grow;
+  // The wavefront's jobs: a touched expert and up to 16 of its tokens, expert
+  // first + wave, + NWV, ...  (beyond 16 tokens in the batch the expert's own
+  // are drawn together first, so few experts need a second job).  Their operands are few but cold, and behind a stream
   // that fills the memory's queues a load takes microseconds: the first job's
   // are read with the first weights, the next one's while a job runs.
   struct Job {
@@ -653,12 +668,24 @@ __global__ __launch_bounds__(NWV * 64) void few_up_kernel(FewArgs a) {
   } job;
   int je = 0, jslot = -1;  // expert, and the slot of the lane's token
   auto job_find = [&](int j) {
-    const int i = first + j / MT, t = 16 * (j % MT) + l;
+    const int i = first + j / MT;
     je = a.elist[1 + i];
-    jslot = t < a.T ? a.eslot[i * FEW_MAX_T + t] : -1;
+    if constexpr (MT == 1) {
+      jslot = l < a.T ? a.eslot[i * FEW_MAX_T + l] : -1;
+    } else {
+      const int slot = lane < a.T ? a.eslot[i * FEW_MAX_T + lane] : -1;
+      const uint32_t m = static_cast<uint32_t>(__ballot(slot >= 0));
+      // the p-th of the expert's tokens to lane p (lanes without one to lane 63)
+      const int to = slot >= 0 ? __popc(m & ((1u << lane) - 1)) : 63;
+      const int packed = __builtin_amdgcn_ds_permute(4 * to, slot);
+      const int from = 16 * (j % MT) + l;
+      const int mine = __shfl(packed, from);
+      jslot = from < __popc(m) ? mine : -1;
+    }
   };
   auto job_load = [&](Job& J) {
     J.slot = jslot;
+    if (MT > 1 && !__any(jslot >= 0)) return;
     J.wgt = a.w[max(jslot, 0)];
     constexpr int es = TY == DT_F32 ? 4 : 2;
     constexpr bool int4r = RS == RS_INT4;
@@ -827,29 +854,25 @@ __global__ __launch_bounds__(NWV * 64) void few_up_kernel(FewArgs a) {
       store_hidden(row, c, wgt * h);
     }
   } else {
-    // The group's touched experts, one (expert, tile of tokens) at a time per
-    // wavefront, everything transposed: MFMA rows are the 16 columns of f, MFMA
-    // columns the tokens.  z + B u: depth 32 = the 16 rank columns twice, against
-    // the two 16-bit parts of u (4-bit B: codes, the scales in u).  The result's
+    // Everything transposed: MFMA rows are the 16 columns of f, MFMA columns the
+    // job's tokens.  z + B u: depth 32 = the 16 rank columns twice, against the
+    // two 16-bit parts of u (4-bit B: codes, the scales in u).  The result's
     // lane holds 4 columns of f of its token, which is the operand form of
     // 16x16x16 MFMAs, so h goes into V = A_down^T h (16 rank columns by tokens)
-    // from the registers, again in two parts.
-    float hsum[MT][2][4];
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int x = 0; x < 2; ++x)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) hsum[m][x][r] = 0.f;
+    // from the registers, again in two parts.  The weighted h go to LDS, one
+    // row per (token, expert), to be summed per token.
+    float* hw = red;  // [tokens of the group][ke][FT]
     for (int j = wave; j < jobs; j += NWV) {
-      const int mt = j % MT, e = je, t = 16 * mt + l;
+      const int e = je;
       const Job J = job;
+      const bool on = J.slot >= 0;
+      const int t = on ? div_small(J.slot, a.over_k) : 0;
       // u, then the next job's operands behind it
       float u[2][8];
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const float* up =
-            a.U + (static_cast<long>(min(t, a.T - 1)) * a.E + e) * Pin * 16 + (Pin == 2 ? x : 0) * 16 + 8 * (q & 1);
+            a.U + (static_cast<long>(t) * a.E + e) * Pin * 16 + (Pin == 2 ? x : 0) * 16 + 8 * (q & 1);
         const f4v u0 = *reinterpret_cast<const f4v*>(up), u1 = *reinterpret_cast<const f4v*>(up + 4);
 #pragma unroll
         for (int r = 0; r < 8; ++r) u[x][r] = r < 4 ? u0[r] : u1[r - 4];
@@ -858,7 +881,7 @@ __global__ __launch_bounds__(NWV * 64) void few_up_kernel(FewArgs a) {
         job_find(j + NWV);
         job_load(job);
       }
-      if (!__any(J.slot >= 0)) continue;
+      if (!__any(on)) continue;
       const int part = q >> 1;
       float hv[2][4];
 #pragma unroll
@@ -880,14 +903,14 @@ __global__ __launch_bounds__(NWV * 64) void few_up_kernel(FewArgs a) {
         } else {
           bw = __builtin_bit_cast(B, J.b[x][0]);
         }
-        B bu = to_frag<TY>(u[x]);
+        B bu = round_frag<TY>(u[x]);
         if constexpr (TY == DT_F32) {
           if (part) bu = zero_frag<TY>();
         } else {
           float rest[8];
 #pragma unroll
           for (int r = 0; r < 8; ++r) rest[r] = u[x][r] - static_cast<float>(bu[r]);
-          const u4v hi = __builtin_bit_cast(u4v, bu), lo = __builtin_bit_cast(u4v, to_frag<TY>(rest));
+          const u4v hi = __builtin_bit_cast(u4v, bu), lo = __builtin_bit_cast(u4v, round_frag<TY>(rest));
           bu = __builtin_bit_cast(B, part ? lo : hi);
         }
         const f4v zz = mfma16<TY>(bw, bu, *reinterpret_cast<const f4v*>(&z[x][t][4 * q]));
@@ -902,9 +925,11 @@ __global__ __launch_bounds__(NWV * 64) void few_up_kernel(FewArgs a) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const float h = Pin == 2 ? silu_f(hv[0][r]) * hv[1][r] : gelu_tanh_f(hv[x][r]);
-          hv[x][r] = J.slot >= 0 ? J.wgt * h : 0.f;
-#pragma unroll
-          for (int m = 0; m < MT; ++m) hsum[m][x][r] += m == mt ? hv[x][r] : 0.f;
+          hv[x][r] = on ? J.wgt * h : 0.f;
+        }
+        if (on) {
+          const int row = div_small(J.slot, a.over_ke), at = __popc(members & ((1u << t) - 1)) * a.ke + (J.slot - row * a.ke);
+          *reinterpret_cast<f4v*>(hw + at * FT + 16 * x + 4 * q) = f4v{hv[x][0], hv[x][1], hv[x][2], hv[x][3]};
         }
         v = down_factor<TY, RS>(J.ad[x], hv[x], v);
       }
@@ -912,26 +937,13 @@ __global__ __launch_bounds__(NWV * 64) void few_up_kernel(FewArgs a) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) v[r] *= scale_at(J.as, r);
       }
-      if (J.slot >= 0) *reinterpret_cast<f4v*>(a.Vp + (static_cast<long>(fb) * a.T * a.k + J.slot) * 16 + 4 * q) = v;
+      if (on) *reinterpret_cast<f4v*>(a.Vp + (static_cast<long>(fb) * a.T * a.k + J.slot) * 16 + 4 * q) = v;
     }
-    // sum over the wavefronts' experts: [wave][m][16 tokens][FT columns]
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        if (Pin == 2 && x == 1) break;
-        f4v o;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) o[r] = hsum[m][x][r];
-        *reinterpret_cast<f4v*>(red + ((wave * MT + m) * 16 + l) * FT + 16 * x + 4 * q) = o;
-      }
     __syncthreads();
     for (int v = threadIdx.x; v < n * FT; v += NWV * 64) {
-      const int c = v % FT, i = v / FT;
-      const int t = srow[i] >> 16, row = srow[i] & 0xFFFF;
+      const int c = v % FT, i = v / FT, row = srow[i] & 0xFFFF;
       float s = 0.f;
-      const int used = min(jobs, NWV);
-      for (int w = 0; w < used; ++w) s += red[((w * MT + (t >> 4)) * 16 + (t & 15)) * FT + c];
+      for (int b = 0; b < a.ke; ++b) s += hw[(i * a.ke + b) * FT + c];
       store_hidden(row, c, s);
     }
   }
@@ -1094,13 +1106,13 @@ __global__ __launch_bounds__(NT) void few_down_kernel(FewArgs a) {
           v[r] *= f16_bits_to_f32(static_cast<uint16_t>((w >> (16 * (r & 1))) & 0xFFFFu));
         }
       }
-      const B hi = to_frag<TY>(v);
+      const B hi = round_frag<TY>(v);
       if constexpr (planes == 1) {
         acc[m] = mfma16<TY>(hi, b, acc[m]);
       } else {
 #pragma unroll
         for (int r = 0; r < 8; ++r) rest[r] = v[r] - static_cast<float>(hi[r]);
-        const B lo = to_frag<TY>(rest);
+        const B lo = round_frag<TY>(rest);
         if constexpr (packed) {
           const u4v x = __builtin_bit_cast(u4v, hi), y = __builtin_bit_cast(u4v, lo);
           acc[0] = mfma16<TY>(__builtin_bit_cast(B, l < 8 ? x : y), b, acc[0]);
@@ -1290,14 +1302,16 @@ template <int XT, int TY, bool Q4, int RS, int MT>
 hipError_t up_mt(const FewArgs& a, hipStream_t st) {
   const unsigned grid = static_cast<unsigned>(a.G < a.T * a.kg ? a.G : a.T * a.kg) * (a.f * a.Pin / 32);
   const size_t lds = sizeof(float) * 2 * MT * 256;  // per wavefront
+  const size_t hw = RS == RS_NONE ? 0 : sizeof(float) * a.T * a.ke * (32 / a.Pin);
+  auto most = [](size_t x, size_t y) { return x > y ? x : y; };
   // More workgroups than compute units: smaller ones, so that one's expert
   // steps overlap the others' streams and the last round is finer.  Without a
   // residual there are no steps and 8 wavefronts keep the longer stream.
   // Measured (us a pass, 4 / 8 / 16 wavefronts): INT4 layer T = 16 89 / 91 /
   // 106, fp16 layer T = 5 33.0 / 34.2 / 41, flat layer T = 2 236 / 229 / 239.
   constexpr int W = RS == RS_NONE ? 8 : 4;
-  if (grid > 256) return go(few_up_kernel<XT, TY, Q4, RS, MT, W>, grid, W * 64, W * lds, a, st);
-  return go(few_up_kernel<XT, TY, Q4, RS, MT, 16>, grid, 1024, 16 * lds, a, st);
+  if (grid > 256) return go(few_up_kernel<XT, TY, Q4, RS, MT, W>, grid, W * 64, most(W * lds, hw), a, st);
+  return go(few_up_kernel<XT, TY, Q4, RS, MT, 16>, grid, 1024, most(16 * lds, hw), a, st);
 }
 
 template <int XT, int TY, bool Q4, int RS>
@@ -1330,11 +1344,10 @@ hipError_t pass(const FewArgs& a, hipStream_t st) {
 
 }  // namespace
 
-int few_router_splits(int d, int NCp) {
-  // at most 16 columns that one workgroup reads in a few microseconds need no
-  // exchange of scores; else two 32-deep units per wavefront keep the matrix's
-  // loads in flight, with at most 4 parts for the selection to add
-  if (NCp == 32 && d <= 8192) return 1;
+int few_router_splits(int d) {
+  // two 32-deep units per wavefront keep the matrix's loads in flight, with at
+  // most 4 parts for the selection to add (one workgroup with the whole depth
+  // of a 4096 x 8 router needs no exchange of scores but reads for 7.5 us)
   const int s = d / 32 / (2 * NW);
   return s < 1 ? 1 : s > 4 ? 4 : s;
 }

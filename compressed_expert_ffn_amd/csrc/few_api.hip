@@ -48,7 +48,8 @@ int create_few(moe_handle* h) {
     s.glist = reinterpret_cast<int*>(take(sizeof(int)));
     s.grec = reinterpret_cast<int4*>(take(sizeof(int4) * std::min<size_t>(c.G, T * kg)));
     s.grow = reinterpret_cast<int16_t*>(take(sizeof(int16_t) * std::min<size_t>(c.G, T * kg) * FEW_MAX_T));
-    s.L = reinterpret_cast<float*>(take(sizeof(float) * few_router_splits(c.d, h->NCp) * T * h->NCp));
+    s.bias = reinterpret_cast<float*>(take(sizeof(float) * h->NCp));
+    s.L = reinterpret_cast<float*>(take(sizeof(float) * few_router_splits(c.d) * T * h->NCp));
     s.elist = reinterpret_cast<int*>(take(sizeof(int) * (1 + std::min<size_t>(h->E, T * h->k))));
     s.eslot = reinterpret_cast<int16_t*>(take(sizeof(int16_t) * std::min<size_t>(h->E, T * h->k) * FEW_MAX_T));
     if (c.r > 0) {
@@ -61,6 +62,13 @@ int create_few(moe_handle* h) {
   carve();
   TRY(dalloc(h, &base, off));
   carve();
+  // biases of the score columns, zeros where the layer has none
+  if (hipMemset(s.bias, 0, sizeof(float) * h->NCp) != hipSuccess ||
+      (h->gbias && hipMemcpy(s.bias, h->gbias, sizeof(float) * c.G, hipMemcpyDeviceToDevice) != hipSuccess) ||
+      (h->ebias && hipMemcpy(s.bias + c.G, h->ebias, sizeof(float) * h->E, hipMemcpyDeviceToDevice) != hipSuccess)) {
+    (void)hipGetLastError();
+    return fail(MOE_ERR_HIP, "initialising the few-token workspace failed");
+  }
   char* zero = static_cast<char*>(s.H) + hidden_row_bytes(h) * T * kg;
   if (hipMemset(s.ticket, 0, sizeof(int)) != hipSuccess || hipMemset(zero, 0, hidden_row_bytes(h)) != hipSuccess ||
       (s.V && hipMemset(s.V + T * h->k * RPAD, 0, RPAD * sizeof(float)) != hipSuccess)) {
@@ -107,9 +115,13 @@ extern "C" int moe_forward_few(moe_handle* h, const void* X, int32_t T, void* Y,
   a.act = c.act == MOE_ACT_SWIGLU ? ACT_SWIGLU : ACT_GELU;
   a.Wr = h->Wr;
   a.NCp = h->NCp;
-  a.nsplit = few_router_splits(c.d, h->NCp);
-  a.gbias = h->gbias;
-  a.ebias = h->ebias;
+  a.nsplit = few_router_splits(c.d);
+  a.bias = s.bias;
+  auto over = [](int n) { return static_cast<uint32_t>(((1ull << 32) + n - 1) / n); };  // 0 for n = 1
+  a.over_nc = over(c.G + (c.K > 1 ? h->E : 0));
+  a.over_kg = over(c.top_groups);
+  a.over_ke = over(c.top_experts);
+  a.over_k = over(h->k);
   a.L = s.L;
   a.ticket = s.ticket;
   a.idx = routing && routing->idx ? routing->idx : s.idx;

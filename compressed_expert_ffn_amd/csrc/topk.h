@@ -4,34 +4,47 @@
 
 namespace cefn {
 
-// Wavefront top-k (higher score first, ties to
-// the lower index, NaN as -inf).  Up to 64 candidates: lane c ranks
-// candidate c by counting the candidates ahead of it.  More: candidate c
-// sits on lane c % 64 and each round takes the best remaining one by a
-// butterfly over the lanes.  Selection r ends up in lane r's (myv, myi).
-// k <= n, k <= 64.
+// Largest value of a wavefront, by row shifts and row broadcasts (lane 63 ends
+// with it; six dependent VALU steps, no LDS).  No NaNs.
+__device__ __forceinline__ float wave_max(float v) {
+  const int lowest = static_cast<int>(0xFF800000u);  // -inf where a step has no source
+  auto step = [&](float x, auto ctrl, auto rows) {
+    const int o = __builtin_amdgcn_update_dpp(lowest, __float_as_int(x), decltype(ctrl)::value, decltype(rows)::value,
+                                              0xf, false);
+    return fmaxf(x, __int_as_float(o));
+  };
+  using std::integral_constant;
+  v = step(v, integral_constant<int, 0x111>{}, integral_constant<int, 0xf>{});  // row_shr:1
+  v = step(v, integral_constant<int, 0x112>{}, integral_constant<int, 0xf>{});
+  v = step(v, integral_constant<int, 0x114>{}, integral_constant<int, 0xf>{});
+  v = step(v, integral_constant<int, 0x118>{}, integral_constant<int, 0xf>{});
+  v = step(v, integral_constant<int, 0x142>{}, integral_constant<int, 0xa>{});  // row_bcast:15
+  v = step(v, integral_constant<int, 0x143>{}, integral_constant<int, 0xc>{});  // row_bcast:31
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+
+// Wavefront top-k (higher score first, ties to the lower index, NaN as -inf).
+// Up to 64 candidates: one per lane, and each round takes the lowest lane that
+// holds the largest value left.  More: candidate c sits on lane c % 64 and
+// each round takes the best remaining one by a butterfly over the lanes.
+// Selection r ends up in lane r's (myv, myi).  k <= n, k <= 64.
 __device__ inline void wave_topk(const float* sv, int n, int k, int lane, float& myv, int& myi) {
   if (n <= 64) {
-    // one candidate per lane, ranked against all n in that same order (a
-    // total order, so the ranks are 0 .. n-1): no cross-lane rounds
     float v = -INFINITY;
     if (lane < n) {
       v = sv[lane];
       v = (v == v) ? v : -INFINITY;
     }
-    int rank = 0;
-    for (int j = 0; j < n; ++j) {
-      const float u = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), j));
-      rank += (u > v || (u == v && j < lane)) ? 1 : 0;
-    }
+    bool left = lane < n;
     myv = -INFINITY;
     myi = -1;
+#pragma unroll 1
     for (int r = 0; r < k; ++r) {
-      const unsigned long long m = __ballot(lane < n && rank == r);
-      const int c = __ffsll((long long)m) - 1;
-      const float u = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), c));
+      const float best = wave_max(left ? v : -INFINITY);
+      const int c = __ffsll(static_cast<long long>(__ballot(left && v == best))) - 1;
+      if (lane == c) left = false;
       if (lane == r) {
-        myv = u;
+        myv = best;
         myi = c;
       }
     }
