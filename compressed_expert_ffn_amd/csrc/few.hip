@@ -35,6 +35,7 @@ namespace {
 
 constexpr int NW = FEW_WAVES;
 constexpr int NT = NW * 64;
+constexpr int UW = NW / 2;  // wavefronts per block of input factors
 
 // The value a wavefront's lane r (the same for all lanes) holds.
 __device__ __forceinline__ float lane_value(float v, int r) {
@@ -219,7 +220,11 @@ __device__ __forceinline__ float block_sum(const float* red, int row, int col) {
   return s;
 }
 
-// u = x A for the 32 factor columns of block nb of group g.
+// u = x A for the 32 factor columns of block nb of group g, by half a
+// workgroup (8 wavefronts; both halves call it together, real: whether this
+// half has a block).  Two blocks per workgroup: 256 experts' blocks and the
+// scores' workgroups are all resident at once (a workgroup each left some for
+// a second round, 13.8 us the launch).
 //
 // 4-bit factors: a 64-deep unit of the block is 256 words, word 64 q' + 32 h +
 // c for depths 64 u + 32 h + 8 q' .. and column c.  Lane 16 q + l takes words
@@ -229,12 +234,12 @@ __device__ __forceinline__ float block_sum(const float* red, int row, int col) {
 // own; two MFMAs for one, but a fourth of the loads (4-byte loads of each
 // half's 16 columns took 6.4 us of a 256-expert layer's launch).
 template <int XT, int TY, bool INT4, int MT>
-__device__ void u_block(const FewArgs& a, int g, int nb, float* red) {
+__device__ void u_block(const FewArgs& a, int g, int nb, bool real, float* red) {
   using XE = typename Elem<XT>::T;
   using B = typename Frag<TY>::T;
-  const int wave = wave_id(), lane = threadIdx.x & 63, l = lane & 15, q = lane >> 4;
-  const int n64 = a.d / 64;
-  const int u0 = n64 * wave / NW, u1 = n64 * (wave + 1) / NW;
+  const int wave = wave_id() % UW, lane = threadIdx.x & 63, l = lane & 15, q = lane >> 4;
+  const int n64 = real ? a.d / 64 : 0, tid = threadIdx.x % (UW * 64);
+  const int u0 = n64 * wave / UW, u1 = n64 * (wave + 1) / UW;
   const int cols = a.K * a.Pin * 16;  // column (j * Pin + p) * 16 + rho of the group
   const XE* xp[MT];
 #pragma unroll
@@ -305,13 +310,13 @@ __device__ void u_block(const FewArgs& a, int g, int nb, float* red) {
         if (h == 0) *reinterpret_cast<f4v*>(red + ((wave * 4 + i) * MT + m) * 128 + (8 * q + l) * 4) = v;
       }
     __syncthreads();
-    for (int v = threadIdx.x; v < a.T * 32; v += NT) {
+    for (int v = tid; v < (real ? a.T * 32 : 0); v += UW * 64) {
       const int row = v >> 5, col = v & 31, r = row & 15;
       if (nb * 32 + col >= cols) continue;
       const int at = ((col & 3) * MT + (row >> 4)) * 128 + (8 * (r >> 2) + (col >> 2)) * 4 + (r & 3);
       float s = 0.f;
 #pragma unroll
-      for (int w = 0; w < NW; ++w) s += red[w * 4 * MT * 128 + at];
+      for (int w = 0; w < UW; ++w) s += red[w * 4 * MT * 128 + at];
       a.U[(static_cast<long>(row) * a.G + g) * cols + nb * 32 + col] = s * Q4Type<TY>::undo;
     }
   } else {
@@ -356,10 +361,10 @@ __device__ void u_block(const FewArgs& a, int g, int nb, float* red) {
       for (int m = 0; m < MT; ++m)
         *reinterpret_cast<f4v*>(red + ((wave * 2 + c) * MT + m) * 256 + lane * 4) = acc[c][m];
     __syncthreads();
-    for (int v = threadIdx.x; v < a.T * 32; v += NT) {
+    for (int v = tid; v < (real ? a.T * 32 : 0); v += UW * 64) {
       const int row = v >> 5, col = v & 31;
       if (nb * 32 + col >= cols) continue;
-      a.U[(static_cast<long>(row) * a.G + g) * cols + nb * 32 + col] = block_sum<NW, 2, MT>(red, row, col);
+      a.U[(static_cast<long>(row) * a.G + g) * cols + nb * 32 + col] = block_sum<UW, 2, MT>(red, row, col);
     }
   }
 }
@@ -551,7 +556,7 @@ __host__ __device__ inline int select_chunk(int T, int NC) {
 }
 
 // grid: the score blocks (16 columns x nsplit depth parts) first, then with
-// u_all one workgroup per 32 factor columns of every group.
+// u_all one workgroup per two blocks of 32 factor columns of every group.
 template <int XT, int TY, int RS, int MT>
 __global__ __launch_bounds__(NT) void few_route_kernel(FewArgs a) {
   extern __shared__ __attribute__((aligned(16))) float red[];  // partial tiles, then scores; last the lists' tables
@@ -560,8 +565,9 @@ __global__ __launch_bounds__(NT) void few_route_kernel(FewArgs a) {
   const int ncb = (NC + 15) / 16, nsb = ncb * a.nsplit;
   if (static_cast<int>(blockIdx.x) >= nsb) {
     if constexpr (RS != RS_NONE) {
-      const int ub = blockIdx.x - nsb, nbu = (a.K * a.Pin * 16 + 31) / 32;
-      u_block<XT, TY, RS == RS_INT4, MT>(a, ub / nbu, ub % nbu, red);
+      const int nbu = (a.K * a.Pin * 16 + 31) / 32, half = wave_id() / UW;
+      const int ub = 2 * (blockIdx.x - nsb) + half;
+      u_block<XT, TY, RS == RS_INT4, MT>(a, ub / nbu, ub % nbu, ub < a.G * nbu, red + half * UW * 2 * MT * 256);
     }
     return;
   }
@@ -612,24 +618,24 @@ __global__ __launch_bounds__(NT) void few_route_kernel(FewArgs a) {
   }
 }
 
-// U of the chosen experts only: one workgroup per 32 factor columns, idle
-// where none of the columns' experts is chosen.
+// U of the chosen experts only: one workgroup per two blocks of 32 factor
+// columns, idle where none of the columns' experts is chosen.
 template <int XT, int TY, int RS, int MT>
 __global__ __launch_bounds__(NT) void few_u_kernel(FewArgs a) {
   extern __shared__ __attribute__((aligned(16))) float red[];
-  __shared__ int hit;
-  const int nbu = (a.K * a.Pin * 16 + 31) / 32;
-  const int g = blockIdx.x / nbu, nb = blockIdx.x % nbu;
+  __shared__ int hit[2];
+  const int nbu = (a.K * a.Pin * 16 + 31) / 32, half = wave_id() / UW, tid = threadIdx.x % (UW * 64);
+  const int ub = 2 * blockIdx.x + half, g = ub / nbu, nb = ub % nbu;
   const int per = 2 / a.Pin;  // experts per block
-  if (threadIdx.x == 0) hit = 0;
+  if (tid == 0) hit[half] = 0;
   __syncthreads();
-  if (static_cast<int>(threadIdx.x) < a.T * a.k) {
-    const int e = a.idx[threadIdx.x] - (g * a.K + nb * per);
-    if (e >= 0 && e < per) hit = 1;
+  if (ub < a.G * nbu && tid < a.T * a.k) {  // at most 512 slots
+    const int e = a.idx[tid] - (g * a.K + nb * per);
+    if (e >= 0 && e < per) hit[half] = 1;
   }
   __syncthreads();
-  if (!hit) return;
-  u_block<XT, TY, RS == RS_INT4, MT>(a, g, nb, red);
+  if (!hit[0] && !hit[1]) return;
+  u_block<XT, TY, RS == RS_INT4, MT>(a, g, nb, hit[half] != 0, red + half * UW * 2 * MT * 256);
 }
 
 // ------------------------------------------------------------------- up --
@@ -984,7 +990,8 @@ __global__ __launch_bounds__(NT) void few_vsum_kernel(FewArgs a) {
 // tokens that chose the expert (zero for the others).  A 4-bit factor's scale
 // varies along the rank columns, i.e. along the depth, so it multiplies V,
 // which then splits into two 16-bit parts like the hidden sums.
-constexpr int kDownPartials = 16;  // partials of V a thread holds in registers
+constexpr int kDownPartials = 16;  // partials of V a thread reads at a time
+constexpr int kDownBatches = 3;
 
 template <int XT, int TY, bool Q4, int RS, int MT>
 __global__ __launch_bounds__(NT) void few_down_kernel(FewArgs a) {
@@ -1134,15 +1141,18 @@ __global__ __launch_bounds__(NT) void few_down_kernel(FewArgs a) {
       return;
     }
     const int nfb = a.f * a.Pin / 32, parts = NT / nv, p = tid / nv, o = tid - p * nv;
-    float x[kDownPartials];
-#pragma unroll
-    for (int i = 0; i < kDownPartials; ++i) {
-      const int b = p + i * parts;
-      x[i] = p < parts && b < nfb ? a.Vp[static_cast<long>(b) * nv + o] : 0.f;
-    }
     float s = 0.f;
+#pragma unroll 1
+    for (int b0 = p; b0 < nfb; b0 += kDownPartials * parts) {
+      float x[kDownPartials];
 #pragma unroll
-    for (int i = 0; i < kDownPartials; ++i) s += x[i];
+      for (int i = 0; i < kDownPartials; ++i) {
+        const int b = b0 + i * parts;
+        x[i] = p < parts && b < nfb ? a.Vp[static_cast<long>(b) * nv + o] : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < kDownPartials; ++i) s += x[i];
+    }
     vpart[tid] = s;
     __syncthreads();
     if (tid < nv) {
@@ -1284,7 +1294,7 @@ hipError_t go(K kernel, unsigned grid, unsigned threads, size_t lds, const FewAr
 template <int XT, int TY, int RS, int MT>
 hipError_t route_mt(const FewArgs& a, hipStream_t st) {
   const int NC = a.G + (a.K > 1 ? a.G * a.K : 0);
-  const unsigned nsb = (NC + 15) / 16 * a.nsplit, nub = a.G * ((a.K * a.Pin * 16 + 31) / 32);
+  const unsigned nsb = (NC + 15) / 16 * a.nsplit, nub = (a.G * ((a.K * a.Pin * 16 + 31) / 32) + 1) / 2;
   const size_t tiles = static_cast<size_t>(NW) * 2 * MT * 256 * sizeof(float);  // of u_block
   const size_t scores =
       sizeof(float) * (static_cast<size_t>(NW) * MT * 256 + static_cast<size_t>(select_chunk(a.T, NC)) * NC);
@@ -1356,7 +1366,7 @@ bool few_v_sum(const FewArgs& a) {
   const long nv = static_cast<long>(a.T) * a.k * 16, nfb = a.f * a.Pin / 32;
   if (nv > NT) return true;
   const long parts = NT / nv;
-  return (nfb + parts - 1) / parts > kDownPartials;
+  return (nfb + parts - 1) / parts > kDownPartials * kDownBatches;
 }
 
 hipError_t launch_few(int xt, int ty, bool q4, const FewArgs& a, hipStream_t st) {
