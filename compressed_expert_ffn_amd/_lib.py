@@ -38,6 +38,9 @@ class moe_route_out(C.Structure):
         "idx", "w", "gidx", "counts", "offsets", "perm", "gcounts", "goffsets", "gperm")]
 
 
+_ROUTE_FIELDS = tuple(n for n, _ in moe_route_out._fields_)
+
+
 class moe_stats(C.Structure):
     _fields_ = [("stored_params", C.c_int64), ("stored_bytes", C.c_int64),
                 ("dense_equiv_params", C.c_int64)]
@@ -183,6 +186,15 @@ def _stream_ptr(stream):
     return C.c_void_p(s.cuda_stream)
 
 
+def _raw_stream(stream, device: int) -> int:
+    """The stream's handle as a number; a device's current stream without
+    building a Stream object (a microsecond of a short call)."""
+    if stream is not None:
+        return stream.cuda_stream
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
 class Layer:
     """One created layer (a moe_handle) plus torch-side buffer marshalling.
 
@@ -220,6 +232,8 @@ class Layer:
         h = C.c_void_p()
         check(lib.moe_create(C.byref(cfg), C.byref(w), _stream_ptr(None) if on_device else None, C.byref(h)))
         self.h = h
+        self.device = torch.cuda.current_device()
+        self._x_dtype = self._torch_x_dtype()
 
     # ----------------------------------------------------------------------
     def _torch_x_dtype(self):
@@ -239,12 +253,10 @@ class Layer:
 
     @staticmethod
     def _route_struct(bufs):
-        ro = moe_route_out()
-        if bufs is not None:
-            for name, _ in moe_route_out._fields_:
-                t = bufs.get(name)
-                setattr(ro, name, None if t is None else t.data_ptr())
-        return ro
+        if bufs is None:
+            return moe_route_out()
+        get = bufs.get
+        return moe_route_out(*[None if (t := get(name)) is None else t.data_ptr() for name in _ROUTE_FIELDS])
 
     def route(self, X, bufs=None, stream=None):
         T = X.shape[0]
@@ -348,17 +360,19 @@ class Layer:
 
     def forward_few(self, X, Y=None, route_bufs=None, stream=None):
         """moe_forward_few: the layer for up to 32 tokens."""
-        import torch
-        if X.dim() != 2 or X.shape[1] != self.cfg.d or X.dtype != self._torch_x_dtype() or not X.is_contiguous():
-            raise ValueError(f"X: expected contiguous {self._torch_x_dtype()} [T, {self.cfg.d}], got {X.dtype} "
-                             f"{tuple(X.shape)}")
+        T, d = X.shape if X.dim() == 2 else (0, -1)
+        if d != self.cfg.d or X.dtype is not self._x_dtype or X.get_device() != self.device or not X.is_contiguous():
+            raise ValueError(f"X: expected contiguous {self._x_dtype} [T, {self.cfg.d}] on device {self.device}, got "
+                             f"{X.dtype} {tuple(X.shape)} on {X.device}")
         if Y is None:
-            Y = torch.empty_like(X)
-        elif Y.shape != X.shape or Y.dtype != X.dtype or not Y.is_contiguous() or Y.device != X.device:
+            Y = X.new_empty((T, d))
+        elif Y.shape != X.shape or Y.dtype is not X.dtype or not Y.is_contiguous() or Y.get_device() != self.device:
             raise ValueError(f"Y: expected contiguous {X.dtype} {tuple(X.shape)} on {X.device}, got {Y.dtype} "
                              f"{tuple(Y.shape)} on {Y.device}")
         rop = None if route_bufs is None else C.byref(self._route_struct(route_bufs))
-        check(lib.moe_forward_few(self.h, X.data_ptr(), X.shape[0], Y.data_ptr(), rop, _stream_ptr(stream)))
+        rc = lib.moe_forward_few(self.h, X.data_ptr(), T, Y.data_ptr(), rop, _raw_stream(stream, self.device))
+        if rc:
+            check(rc)
         return Y
 
     def debug_residual(self, proj: int, which: int, expert: int):
@@ -403,17 +417,21 @@ class Layer:
 # ------------------------------------------------- products with 4-bit weights --
 def _rows(t, n: int, dtype, name: str, device: int):
     """Row count and row pitch of a 2-D tensor [T, n] with unit column stride."""
-    if t.dim() != 2 or t.shape[1] != n:
-        raise ValueError(f"{name}: expected [T, {n}], got {tuple(t.shape)}")
-    if t.dtype != dtype:
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != n:
+        raise ValueError(f"{name}: expected [T, {n}], got {tuple(shape)}")
+    if t.dtype is not dtype:
         raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
-    if not t.is_cuda or t.device.index != device:
+    if t.get_device() != device:
         raise ValueError(f"{name}: expected a tensor on device {device}, got {t.device}")
-    if t.stride(1) != 1 and n > 1:
+    pitch, step = t.stride()
+    if step != 1 and n > 1:
         raise ValueError(f"{name}: the elements of a row must be consecutive")
-    if t.shape[0] > 1 and t.stride(0) < n:
-        raise ValueError(f"{name}: rows overlap (row pitch {t.stride(0)} < {n})")
-    return t.shape[0], (t.stride(0) if t.shape[0] > 1 else n)
+    if shape[0] <= 1:
+        return shape[0], n
+    if pitch < n:
+        raise ValueError(f"{name}: rows overlap (row pitch {pitch} < {n})")
+    return shape[0], pitch
 
 
 class QuantLinear:
@@ -469,14 +487,15 @@ class QuantLinear:
 
     def matvec(self, X, Y=None, stream=None):
         """Y = X W for X [T, n_in]; rows may be strided."""
-        import torch
         T, ldx = _rows(X, self.n_in, self.dtype, "X", self.device)
         if Y is None:
-            Y = torch.empty((T, self.n_out), dtype=self.dtype, device=X.device)
+            Y = X.new_empty((T, self.n_out))
         Ty, ldy = _rows(Y, self.n_out, self.dtype, "Y", self.device)
         if Ty != T:
             raise ValueError(f"Y has {Ty} rows, X has {T}")
-        check(lib.moe_quant_matvec(self.h, X.data_ptr(), ldx, T, Y.data_ptr(), ldy, _stream_ptr(stream)))
+        rc = lib.moe_quant_matvec(self.h, X.data_ptr(), ldx, T, Y.data_ptr(), ldy, _raw_stream(stream, self.device))
+        if rc:
+            check(rc)
         return Y
 
     def read(self):

@@ -124,46 +124,56 @@ struct MatvecArgs {
   long ldy;
 };
 
-constexpr int kMvWaves = 16;
-
-// grid: one workgroup per tile of 16 C columns; its 16 wavefronts take
+// grid: one workgroup per JT tiles of 16 C columns; its NW wavefronts take
 // consecutive ranges of the units and their sums meet in LDS.  GPU: groups
 // per unit.  ALIGNED: rows of X can be read 16 bytes at a time.
-template <int XT, int C, int GPU, int MT, bool ALIGNED>
-__global__ __launch_bounds__(kMvWaves * 64) void q4_matvec_kernel(MatvecArgs a) {
+template <int XT, int C, int GPU, int MT, int JT, int NW, int R, bool ALIGNED>
+__global__ __launch_bounds__(NW * 64) void q4_matvec_kernel(MatvecArgs a) {
   using B = typename Frag<XT>::T;
   constexpr int UNIT = 128 / C, NS = 4 / C;  // rows, 32-row steps per unit
   constexpr int E = C * GPU;                 // scales per column and unit
   constexpr int SPG = NS / GPU;              // 32-row steps per group
-  __shared__ float red[kMvWaves][C * MT * 256];
+  extern __shared__ __attribute__((aligned(16))) float red[];  // [NW][JT * C][MT][256]
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int l = lane & 15, kq = 8 * (lane >> 4);
   const int nu = static_cast<int>(a.s.units());
-  const int u0 = static_cast<int>(static_cast<long>(nu) * wave / kMvWaves);
-  const int u1 = static_cast<int>(static_cast<long>(nu) * (wave + 1) / kMvWaves);
-  const uint32_t* wp = a.words + static_cast<long>(blockIdx.x) * nu * 256 + lane * 4;
-  const uint16_t* sp = a.scales + (static_cast<long>(blockIdx.x) * a.s.srows() * 16 + l) * E;
+  const int u0 = static_cast<int>(static_cast<long>(nu) * wave / NW);
+  const int u1 = static_cast<int>(static_cast<long>(nu) * (wave + 1) / NW);
+  const int tile0 = blockIdx.x * JT, tiles = static_cast<int>(a.s.tiles());
+  const uint32_t* wp[JT];
+  const uint16_t* sp[JT];
+#pragma unroll
+  for (int j = 0; j < JT; ++j) {
+    const long t = min(tile0 + j, tiles - 1);  // tiles past the last repeat it
+    wp[j] = a.words + t * nu * 256 + lane * 4;
+    sp[j] = a.scales + (t * a.s.srows() * 16 + l) * E;
+  }
   const int su = a.s.srow_units();
   const uint16_t* xp[MT];
 #pragma unroll
   for (int m = 0; m < MT; ++m) xp[m] = a.X + min(16 * m + l, a.T - 1) * a.ldx;  // rows past T repeat the last one
   struct Slot {
-    u4v w;
-    u2v s;  // E fp16 scales
+    u4v w[JT];
+    u2v s[JT];  // E fp16 scales
     u4v x[NS][MT];
   };
-  f4v acc[C][MT];
+  f4v acc[JT][C][MT];
 #pragma unroll
-  for (int c = 0; c < C; ++c)
+  for (int j = 0; j < JT; ++j)
 #pragma unroll
-    for (int m = 0; m < MT; ++m) acc[c][m] = f4v{0.f, 0.f, 0.f, 0.f};
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int m = 0; m < MT; ++m) acc[j][c][m] = f4v{0.f, 0.f, 0.f, 0.f};
   const B ones = q4_ones<XT>();
-  stream_units<(!ALIGNED ? 1 : MT == 1 ? (C == 1 ? 3 : 4) : 2), Slot>(
+  stream_units<ALIGNED ? R : 1, Slot>(
       u1 - u0,
       [&](int i, Slot& s) {
         const int u = u0 + i;
-        s.w = *reinterpret_cast<const u4v*>(wp + static_cast<long>(u) * 256);
-        s.s = load_scales<E>(sp + static_cast<long>(u / su) * 16 * E);
+#pragma unroll
+        for (int j = 0; j < JT; ++j) {
+          s.w[j] = *reinterpret_cast<const u4v*>(wp[j] + static_cast<long>(u) * 256);
+          s.s[j] = load_scales<E>(sp[j] + static_cast<long>(u / su) * 16 * E);
+        }
 #pragma unroll
         for (int st = 0; st < NS; ++st) {
           const int k = u * UNIT + 32 * st + kq;
@@ -174,8 +184,8 @@ __global__ __launch_bounds__(kMvWaves * 64) void q4_matvec_kernel(MatvecArgs a) 
       [&](const Slot& s) {
 #pragma unroll
         for (int g = 0; g < GPU; ++g) {
-          f4v part[C][MT];
           // sum of the group's activations, in every column of the tile
+          f4v off[MT];
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
             f4v sum = {0.f, 0.f, 0.f, 0.f};
@@ -183,62 +193,81 @@ __global__ __launch_bounds__(kMvWaves * 64) void q4_matvec_kernel(MatvecArgs a) 
             for (int st = 0; st < SPG; ++st)
               sum = mfma16<XT>(__builtin_bit_cast(B, s.x[g * SPG + st][m]), ones, sum);
 #pragma unroll
-            for (int c = 0; c < C; ++c)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) part[c][m][i] = -kQ4Offset * sum[i];
+            for (int i = 0; i < 4; ++i) off[m][i] = -kQ4Offset * sum[i];
           }
 #pragma unroll
-          for (int st = 0; st < SPG; ++st)
+          for (int j = 0; j < JT; ++j) {
+            f4v part[C][MT];
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+              for (int m = 0; m < MT; ++m) part[c][m] = off[m];
+#pragma unroll
+            for (int st = 0; st < SPG; ++st)
+#pragma unroll
+              for (int c = 0; c < C; ++c) {
+                const uint32_t word = s.w[j][(g * SPG + st) * C + c];
+                const B b = q4_frag<XT>(word);
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+                  part[c][m] = mfma16<XT>(__builtin_bit_cast(B, s.x[g * SPG + st][m]), b, part[c][m]);
+              }
 #pragma unroll
             for (int c = 0; c < C; ++c) {
-              const uint32_t word = s.w[(g * SPG + st) * C + c];
-              const B b = q4_frag<XT>(word);
+              const float sc = scale_at(s.s[j], g * C + c);
 #pragma unroll
               for (int m = 0; m < MT; ++m)
-                part[c][m] = mfma16<XT>(__builtin_bit_cast(B, s.x[g * SPG + st][m]), b, part[c][m]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[j][c][m][i] += sc * part[c][m][i];
             }
-#pragma unroll
-          for (int c = 0; c < C; ++c) {
-            const float sc = scale_at(s.s, g * C + c);
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) acc[c][m][i] += sc * part[c][m][i];
           }
         }
       });
 #pragma unroll
-  for (int c = 0; c < C; ++c)
+  for (int j = 0; j < JT; ++j)
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-      *reinterpret_cast<f4v*>(&red[wave][((c * MT + m) * 64 + lane) * 4]) = acc[c][m];
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+        *reinterpret_cast<f4v*>(red + (((wave * JT + j) * C + c) * MT + m) * 256 + lane * 4) = acc[j][c][m];
   __syncthreads();
   // row 4 (lane / 16) + i of a block, column lane % 16: consecutive threads
   // take consecutive columns
-  for (int v = threadIdx.x; v < C * 16 * a.T; v += kMvWaves * 64) {
-    const int row = v / (C * 16), col = v % (C * 16);
-    const int n = blockIdx.x * (16 * C) + col;
+  constexpr int COLS = JT * C * 16;
+  for (int v = threadIdx.x; v < COLS * a.T; v += NW * 64) {
+    const int row = v / COLS, col = v % COLS;
+    const int n = blockIdx.x * COLS + col;
     if (n >= a.s.n_out) continue;
     const int r = row & 15;
-    const int at = (((col >> 4) * MT + (row >> 4)) * 64 + 16 * (r >> 2) + (col & 15)) * 4 + (r & 3);
+    const int at = ((col >> 4) * MT + (row >> 4)) * 256 + (16 * (r >> 2) + (col & 15)) * 4 + (r & 3);
     float sum = 0.f;
 #pragma unroll
-    for (int w = 0; w < kMvWaves; ++w) sum += red[w][at];
+    for (int w = 0; w < NW; ++w) sum += red[w * JT * C * MT * 256 + at];
     a.Y[row * a.ldy + n] = from_f32<XT>(sum * Q4Type<XT>::undo);
   }
 }
 
+template <int XT, int C, int GPU, int MT, int JT, int NW, int R>
+hipError_t launch_mv3(const MatvecArgs& a, bool aligned, hipStream_t st) {
+  const dim3 grid(static_cast<unsigned>((a.s.tiles() + JT - 1) / JT)), block(NW * 64);
+  const size_t lds = sizeof(float) * NW * JT * C * MT * 256;
+  auto go = [&](auto kernel) -> hipError_t {
+    if (lds > 64 * 1024) {
+      const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                               hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(lds));
+      if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL(kernel, grid, block, lds, st, a);
+    return hipGetLastError();
+  };
+  return aligned ? go(q4_matvec_kernel<XT, C, GPU, MT, JT, NW, R, true>)
+                 : go(q4_matvec_kernel<XT, C, GPU, MT, JT, NW, R, false>);
+}
+
 template <int XT, int C, int GPU>
 hipError_t launch_mv2(const MatvecArgs& a, bool aligned, hipStream_t st) {
-  const dim3 grid(static_cast<unsigned>(a.s.tiles())), block(kMvWaves * 64);
-  if (a.T <= 16) {
-    if (aligned) hipLaunchKernelGGL((q4_matvec_kernel<XT, C, GPU, 1, true>), grid, block, 0, st, a);
-    else hipLaunchKernelGGL((q4_matvec_kernel<XT, C, GPU, 1, false>), grid, block, 0, st, a);
-  } else {
-    if (aligned) hipLaunchKernelGGL((q4_matvec_kernel<XT, C, GPU, 2, true>), grid, block, 0, st, a);
-    else hipLaunchKernelGGL((q4_matvec_kernel<XT, C, GPU, 2, false>), grid, block, 0, st, a);
-  }
-  return hipGetLastError();
+  if (a.T <= 16) return launch_mv3<XT, C, GPU, 1, 1, 16, C == 1 ? 3 : 4>(a, aligned, st);
+  return launch_mv3<XT, C, GPU, 2, 1, 8, C == 1 ? 4 : C == 2 ? 5 : 6>(a, aligned, st);
 }
 
 template <int XT>
@@ -305,7 +334,7 @@ int validate_quant(const moe_quant_config* c) {
 // every compute unit, since a wide tile re-uses the activations' fragments.
 int pick_c(int n_out) {
   for (int C : {4, 2})
-    if ((n_out + 16 * C - 1) / (16 * C) >= 256) return C;
+    if ((n_out + 16 * C - 1) / (16 * C) >= 192) return C;
   return 1;
 }
 
