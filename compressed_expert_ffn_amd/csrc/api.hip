@@ -269,6 +269,7 @@ int build_base_on_device(moe_handle* h, const moe_weights* w, bool on_device) {
   }
   const Q4Shape s1{d, Pin * f, 2, 32}, s2{f, d, 1, 32};
   uint32_t *w1 = nullptr, *w2 = nullptr;
+  h->w1_units = (int)s1.units();
   h->w1_gs = s1.words();
   h->w2_gs = s2.words();
   h->w1_sgs = s1.scales();

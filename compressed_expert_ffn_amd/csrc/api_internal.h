@@ -66,6 +66,7 @@ struct moe_handle {
   uint16_t *At_s = nullptr, *B1_s = nullptr, *Ad_s = nullptr, *Bd_s = nullptr;
   uint16_t *W1_s = nullptr, *W2_s = nullptr;  // scales of a 4-bit base
   long w1_sgs = 0, w2_sgs = 0;
+  int w1_units = 0;  // units per tile of a 4-bit W1
   long w1_gs = 0, w2_gs = 0, at_gs = 0, at_sgs = 0, bd_gs = 0;
   Workspace ws;         // the handle's own workspace, carved for T_max
   int nt1 = 0;          // column tiles of gemm1 (partials of V per row)

@@ -50,6 +50,7 @@ struct FewArgs {
   long w1_gs, w2_gs;             // per group: elements, or 32-bit words of a 4-bit base
   const uint16_t *W1_s, *W2_s;   // 4-bit base: scales
   long w1_sgs, w2_sgs;
+  int w1_units;   // 4-bit base: units per tile of W1
   const void *B1, *Ad, *Bd;
   long bd_gs;
   int NV;

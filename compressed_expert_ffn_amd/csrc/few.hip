@@ -735,8 +735,8 @@ __global__ __launch_bounds__(NWV * 64) void few_up_kernel(FewArgs a) {
     for (int m = 0; m < MT; ++m) acc[c][m] = f4v{0.f, 0.f, 0.f, 0.f};
   if constexpr (Q4) {
     const uint32_t* wp =
-        static_cast<const uint32_t*>(a.W1) + g * a.w1_gs + (static_cast<long>(fb) * n64 * 64 + lane) * 4;
-    const uint16_t* sp = a.W1_s + g * a.w1_sgs + (static_cast<long>(fb) * n64 * 16 + l) * 4;
+        static_cast<const uint32_t*>(a.W1) + g * a.w1_gs + (static_cast<long>(fb) * a.w1_units * 64 + lane) * 4;
+    const uint16_t* sp = a.W1_s + g * a.w1_sgs + (static_cast<long>(fb) * a.w1_units * 16 + l) * 4;
     struct Slot {
       Raw<XT> x[2][MT];
       u4v w;

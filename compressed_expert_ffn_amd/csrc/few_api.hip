@@ -153,6 +153,7 @@ extern "C" int moe_forward_few(moe_handle* h, const void* X, int32_t T, void* Y,
   a.W1_s = h->W1_s;
   a.W2_s = h->W2_s;
   a.w1_sgs = h->w1_sgs;
+  a.w1_units = h->w1_units;
   a.w2_sgs = h->w2_sgs;
   a.B1 = h->B1;
   a.Ad = h->Ad;

@@ -121,7 +121,7 @@ struct Q4Shape {
   int n_in, n_out, C, group;
   __host__ __device__ int unit() const { return 128 / C; }
   __host__ __device__ long tiles() const { return (n_out + 16 * C - 1) / (16 * C); }
-  __host__ __device__ long units() const { return (n_in + unit() - 1) / unit(); }
+  __host__ __device__ long units() const { return (n_in + 127L) / 128 * C; }  // whole runs of 128 rows
   __host__ __device__ int srow_units() const { return group > unit() ? group / unit() : 1; }  // units per scale row
   __host__ __device__ long srows() const { return (units() + srow_units() - 1) / srow_units(); }
   __host__ __device__ int gpu() const { return group >= unit() ? 1 : unit() / group; }  // groups per unit

@@ -124,84 +124,93 @@ struct MatvecArgs {
   long ldy;
 };
 
-// grid: one workgroup per JT tiles of 16 C columns; its NW wavefronts take
-// consecutive ranges of the units and their sums meet in LDS.  GPU: groups
-// per unit.  ALIGNED: rows of X can be read 16 bytes at a time.
-template <int XT, int C, int GPU, int MT, int JT, int NW, int R, bool ALIGNED>
+// grid: one workgroup per tile of 16 C columns; its NW wavefronts take
+// consecutive ranges of 128-deep runs (C units each) and their sums meet in
+// LDS.  GPU: groups per unit.  XI: loads of x per run, 4 rows each, so at most
+// 4 XI rows.  ALIGNED: rows of X can be read 16 bytes at a time.
+//
+// A run of x is read the way memory holds it, 16 lanes to the 256 bytes of a
+// row, and goes through the wavefront's own part of LDS to become operands
+// (row on lane % 16).  Read as operands directly, 64 bytes of 16 rows, each
+// load touches 16 lines for half of each; a compute unit takes about 2.5
+// clocks a line, which bound every product of several rows (14336 x 4096,
+// 32 rows: 31 us), and one row still cost the loads of 16.
+template <int XT, int C, int GPU, int XI, int NW, int R, bool ALIGNED>
 __global__ __launch_bounds__(NW * 64) void q4_matvec_kernel(MatvecArgs a) {
   using B = typename Frag<XT>::T;
-  constexpr int UNIT = 128 / C, NS = 4 / C;  // rows, 32-row steps per unit
+  constexpr int MT = (4 * XI + 15) / 16;     // tiles of 16 rows
+  constexpr int NS = 4 / C;                  // 32-row steps per unit
   constexpr int E = C * GPU;                 // scales per column and unit
   constexpr int SPG = NS / GPU;              // 32-row steps per group
-  extern __shared__ __attribute__((aligned(16))) float red[];  // [NW][JT * C][MT][256]
+  constexpr int PITCH = 272;                 // bytes of a row of x in LDS: 16 past a multiple of 128
+  constexpr int XROWS = 16 * MT;
+  extern __shared__ __attribute__((aligned(16))) char lds[];  // x [NW][XROWS][PITCH]; later sums [NW][C][MT][256]
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int l = lane & 15, kq = 8 * (lane >> 4);
-  const int nu = static_cast<int>(a.s.units());
-  const int u0 = static_cast<int>(static_cast<long>(nu) * wave / NW);
-  const int u1 = static_cast<int>(static_cast<long>(nu) * (wave + 1) / NW);
-  const int tile0 = blockIdx.x * JT, tiles = static_cast<int>(a.s.tiles());
-  const uint32_t* wp[JT];
-  const uint16_t* sp[JT];
-#pragma unroll
-  for (int j = 0; j < JT; ++j) {
-    const long t = min(tile0 + j, tiles - 1);  // tiles past the last repeat it
-    wp[j] = a.words + t * nu * 256 + lane * 4;
-    sp[j] = a.scales + (t * a.s.srows() * 16 + l) * E;
-  }
+  const int l = lane & 15, q = lane >> 4;
+  const int runs = static_cast<int>(a.s.units()) / C;
+  const int u0 = static_cast<int>(static_cast<long>(runs) * wave / NW);
+  const int u1 = static_cast<int>(static_cast<long>(runs) * (wave + 1) / NW);
+  const uint32_t* wp = a.words + static_cast<long>(blockIdx.x) * a.s.units() * 256 + lane * 4;
+  const uint16_t* sp = a.scales + (static_cast<long>(blockIdx.x) * a.s.srows() * 16 + l) * E;
   const int su = a.s.srow_units();
-  const uint16_t* xp[MT];
+  // lane 16 r + c of load i: row 4 i + r, depths 8 c .. of the run
+  const uint16_t* xp[XI];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) xp[m] = a.X + min(16 * m + l, a.T - 1) * a.ldx;  // rows past T repeat the last one
+  for (int i = 0; i < XI; ++i) xp[i] = a.X + min(4 * i + q, a.T - 1) * a.ldx;  // rows past T repeat the last one
+  char* xw = lds + wave * XROWS * PITCH + q * PITCH + l * 16;
+  const char* xr = lds + wave * XROWS * PITCH + min(l, 4 * XI - 1) * PITCH + q * 16;
   struct Slot {
-    u4v w[JT];
-    u2v s[JT];  // E fp16 scales
-    u4v x[NS][MT];
+    u4v w[C];
+    u2v s[C];  // E fp16 scales
+    u4v x[XI];
   };
-  f4v acc[JT][C][MT];
+  f4v acc[C][MT];
 #pragma unroll
-  for (int j = 0; j < JT; ++j)
+  for (int c = 0; c < C; ++c)
 #pragma unroll
-    for (int c = 0; c < C; ++c)
-#pragma unroll
-      for (int m = 0; m < MT; ++m) acc[j][c][m] = f4v{0.f, 0.f, 0.f, 0.f};
+    for (int m = 0; m < MT; ++m) acc[c][m] = f4v{0.f, 0.f, 0.f, 0.f};
   const B ones = q4_ones<XT>();
   stream_units<ALIGNED ? R : 1, Slot>(
       u1 - u0,
       [&](int i, Slot& s) {
-        const int u = u0 + i;
+        const int run = u0 + i;
 #pragma unroll
-        for (int j = 0; j < JT; ++j) {
-          s.w[j] = *reinterpret_cast<const u4v*>(wp[j] + static_cast<long>(u) * 256);
-          s.s[j] = load_scales<E>(sp[j] + static_cast<long>(u / su) * 16 * E);
+        for (int j = 0; j < C; ++j) {
+          const int u = run * C + j;
+          s.w[j] = *reinterpret_cast<const u4v*>(wp + static_cast<long>(u) * 256);
+          s.s[j] = load_scales<E>(sp + static_cast<long>(u / su) * 16 * E);
         }
 #pragma unroll
-        for (int st = 0; st < NS; ++st) {
-          const int k = u * UNIT + 32 * st + kq;
-#pragma unroll
-          for (int m = 0; m < MT; ++m) s.x[st][m] = load_row8<ALIGNED>(xp[m], k, a.s.n_in);
-        }
+        for (int j = 0; j < XI; ++j) s.x[j] = load_row8<ALIGNED>(xp[j], run * 128 + 8 * l, a.s.n_in);
       },
       [&](const Slot& s) {
+        // the wavefront's LDS operations run in order, so its reads see its
+        // writes and the next run's writes come after them
 #pragma unroll
-        for (int g = 0; g < GPU; ++g) {
-          // sum of the group's activations, in every column of the tile
-          f4v off[MT];
+        for (int j = 0; j < XI; ++j) *reinterpret_cast<u4v*>(xw + 4 * j * PITCH) = s.x[j];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
 #pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            f4v sum = {0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < C; ++j) {
 #pragma unroll
-            for (int st = 0; st < SPG; ++st)
-              sum = mfma16<XT>(__builtin_bit_cast(B, s.x[g * SPG + st][m]), ones, sum);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) off[m][i] = -kQ4Offset * sum[i];
-          }
-#pragma unroll
-          for (int j = 0; j < JT; ++j) {
+          for (int g = 0; g < GPU; ++g) {
+            B x[SPG][MT];
             f4v part[C][MT];
+            // sum of the group's activations, in every column of the tile
 #pragma unroll
-            for (int c = 0; c < C; ++c)
+            for (int m = 0; m < MT; ++m) {
+              f4v sum = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-              for (int m = 0; m < MT; ++m) part[c][m] = off[m];
+              for (int st = 0; st < SPG; ++st) {
+                const int step = j * NS + g * SPG + st;
+                x[st][m] = __builtin_bit_cast(B, *reinterpret_cast<const u4v*>(xr + 16 * m * PITCH + step * 64));
+                sum = mfma16<XT>(x[st][m], ones, sum);
+              }
+#pragma unroll
+              for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) part[c][m][i] = -kQ4Offset * sum[i];
+            }
 #pragma unroll
             for (int st = 0; st < SPG; ++st)
 #pragma unroll
@@ -209,8 +218,7 @@ __global__ __launch_bounds__(NW * 64) void q4_matvec_kernel(MatvecArgs a) {
                 const uint32_t word = s.w[j][(g * SPG + st) * C + c];
                 const B b = q4_frag<XT>(word);
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
-                  part[c][m] = mfma16<XT>(__builtin_bit_cast(B, s.x[g * SPG + st][m]), b, part[c][m]);
+                for (int m = 0; m < MT; ++m) part[c][m] = mfma16<XT>(x[st][m], b, part[c][m]);
               }
 #pragma unroll
             for (int c = 0; c < C; ++c) {
@@ -218,22 +226,24 @@ __global__ __launch_bounds__(NW * 64) void q4_matvec_kernel(MatvecArgs a) {
 #pragma unroll
               for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[j][c][m][i] += sc * part[c][m][i];
+                for (int i = 0; i < 4; ++i) acc[c][m][i] += sc * part[c][m][i];
             }
           }
         }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
       });
+  __syncthreads();  // every wavefront is done with its x: the sums take its place
+  float* red = reinterpret_cast<float*>(lds);
 #pragma unroll
-  for (int j = 0; j < JT; ++j)
+  for (int c = 0; c < C; ++c)
 #pragma unroll
-    for (int c = 0; c < C; ++c)
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-        *reinterpret_cast<f4v*>(red + (((wave * JT + j) * C + c) * MT + m) * 256 + lane * 4) = acc[j][c][m];
+    for (int m = 0; m < MT; ++m)
+      *reinterpret_cast<f4v*>(red + ((wave * C + c) * MT + m) * 256 + lane * 4) = acc[c][m];
   __syncthreads();
   // row 4 (lane / 16) + i of a block, column lane % 16: consecutive threads
   // take consecutive columns
-  constexpr int COLS = JT * C * 16;
+  constexpr int COLS = C * 16;
   for (int v = threadIdx.x; v < COLS * a.T; v += NW * 64) {
     const int row = v / COLS, col = v % COLS;
     const int n = blockIdx.x * COLS + col;
@@ -242,15 +252,17 @@ __global__ __launch_bounds__(NW * 64) void q4_matvec_kernel(MatvecArgs a) {
     const int at = ((col >> 4) * MT + (row >> 4)) * 256 + (16 * (r >> 2) + (col & 15)) * 4 + (r & 3);
     float sum = 0.f;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) sum += red[w * JT * C * MT * 256 + at];
+    for (int w = 0; w < NW; ++w) sum += red[w * C * MT * 256 + at];
     a.Y[row * a.ldy + n] = from_f32<XT>(sum * Q4Type<XT>::undo);
   }
 }
 
-template <int XT, int C, int GPU, int MT, int JT, int NW, int R>
+template <int XT, int C, int GPU, int XI, int NW, int R>
 hipError_t launch_mv3(const MatvecArgs& a, bool aligned, hipStream_t st) {
-  const dim3 grid(static_cast<unsigned>((a.s.tiles() + JT - 1) / JT)), block(NW * 64);
-  const size_t lds = sizeof(float) * NW * JT * C * MT * 256;
+  constexpr int MT = (4 * XI + 15) / 16;
+  const dim3 grid(static_cast<unsigned>(a.s.tiles())), block(NW * 64);
+  constexpr size_t xb = static_cast<size_t>(NW) * 16 * MT * 272, sb = sizeof(float) * NW * C * MT * 256;
+  constexpr size_t lds = xb > sb ? xb : sb;
   auto go = [&](auto kernel) -> hipError_t {
     if (lds > 64 * 1024) {
       const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
@@ -260,14 +272,21 @@ hipError_t launch_mv3(const MatvecArgs& a, bool aligned, hipStream_t st) {
     hipLaunchKernelGGL(kernel, grid, block, lds, st, a);
     return hipGetLastError();
   };
-  return aligned ? go(q4_matvec_kernel<XT, C, GPU, MT, JT, NW, R, true>)
-                 : go(q4_matvec_kernel<XT, C, GPU, MT, JT, NW, R, false>);
+  return aligned ? go(q4_matvec_kernel<XT, C, GPU, XI, NW, R, true>)
+                 : go(q4_matvec_kernel<XT, C, GPU, XI, NW, R, false>);
 }
 
 template <int XT, int C, int GPU>
 hipError_t launch_mv2(const MatvecArgs& a, bool aligned, hipStream_t st) {
-  if (a.T <= 16) return launch_mv3<XT, C, GPU, 1, 1, 16, C == 1 ? 3 : 4>(a, aligned, st);
-  return launch_mv3<XT, C, GPU, 2, 1, 8, C == 1 ? 4 : C == 2 ? 5 : 6>(a, aligned, st);
+  // Narrow tiles: about one workgroup per compute unit, which 16 wavefronts
+  // fill; wide ones: more workgroups or more loads per run, 8 wavefronts and
+  // deeper rings.  Measured (us, 8 / 16 wavefronts): 4096 x 4096, 1 row 5.3 /
+  // 4.9, 32 rows 9.9 / 8.6; 4096 x 14336, 1 row 10.0 / 10.1, 32 rows 15.8 / 21.4.
+  constexpr int W = C == 1 ? 16 : 8;
+  if (a.T <= 4) return launch_mv3<XT, C, GPU, 1, W, C == 4 ? 2 : C == 2 ? 4 : 3>(a, aligned, st);
+  if (a.T <= 8) return launch_mv3<XT, C, GPU, 2, W, C == 4 ? 2 : C == 2 ? 4 : 2>(a, aligned, st);
+  if (a.T <= 16) return launch_mv3<XT, C, GPU, 4, W, C == 4 ? 2 : C == 2 ? 3 : 1>(a, aligned, st);
+  return launch_mv3<XT, C, GPU, 8, W, C == 4 ? 2 : C == 2 ? 3 : 1>(a, aligned, st);
 }
 
 template <int XT>
@@ -330,8 +349,11 @@ int validate_quant(const moe_quant_config* c) {
   return MOE_OK;
 }
 
-// Columns per tile (16 C): the widest tile that still leaves a workgroup for
-// every compute unit, since a wide tile re-uses the activations' fragments.
+// Columns per tile (16 C): the widest tile that still gives most compute units
+// a workgroup, since a wide tile re-uses the activations' fragments.  8192 x
+// 28672 in tiles of 64 / 32 / 16 columns: 46 / 58 / 76 us for 24 rows, 27.7 /
+// 26.4 / 25.3 us for one; 4096 x 14336: 15.9 / 22.1 / 31.8 us for 32 rows,
+// 9.8 / 9.1 / 9.6 us for one.
 int pick_c(int n_out) {
   for (int C : {4, 2})
     if ((n_out + 16 * C - 1) / (16 * C) >= 192) return C;
