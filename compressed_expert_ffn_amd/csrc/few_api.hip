@@ -145,7 +145,13 @@ extern "C" int moe_forward_few(moe_handle* h, const void* X, int32_t T, void* Y,
   a.at_sgs = h->at_sgs;
   a.NU = h->NU;
   a.U = s.U;
-  a.u_all = 1;
+  // The input factors of every expert are read beside the selection while they
+  // take no longer than it and the launch that reading the chosen ones' alone
+  // costs.  Measured, one token, every / chosen: 19 MB 32.8 / 39.7 us a pass,
+  // 67 MB 41.0 / 34.1, 75 MB in 4 bits 63 / 46, 134 MB 71 / 45.
+  const size_t factors = (size_t)c.G * (c.resid == MOE_RESID_INT4_G32 ? 4 * h->at_gs + 2 * h->at_sgs
+                                                                      : elem_bytes(h->mma) * h->at_gs);
+  a.u_all = factors <= ((size_t)40 << 20) ? 1 : 0;
   a.W1 = h->W1;
   a.W2 = h->W2;
   a.w1_gs = h->w1_gs;

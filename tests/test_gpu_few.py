@@ -106,6 +106,10 @@ CASES = [
     ("swiglu", "f16", "f16", "int4_g32", 2, (16, 64), 2, 8, 32, 64, 64),
     ("swiglu", "bf16", "bf16", "none", 0, (256, 4), 8, 2, 32, 64, 64),
     ("gelu_tanh", "f32", "f32", "none", 0, (4, 256), 1, 16, 11, 64, 64),
+    # input factors past 40 MB: only the chosen experts' are read, by a launch of their own
+    ("swiglu", "f16", "f16", "f16", 16, (16, 64), 2, 8, 5, 704, 64),
+    ("gelu_tanh", "f32", "f32", "f32", 16, (16, 64), 2, 4, 20, 704, 64),
+    ("swiglu", "bf16", "bf16", "int4_g32", 16, (16, 64), 1, 8, 17, 2560, 64),
 ]
 
 
