@@ -42,7 +42,6 @@ struct FewArgs {
   const void* At;
   const uint16_t* At_s;
   long at_gs, at_sgs;
-  int NU;
   float* U;       // [T][E][Pin][16]
   int u_all;      // U of every expert, in the scores' launch; 0: of the chosen ones, in a launch of its own
   // weights (layouts in kernels.h; 4-bit bases in q4.h)

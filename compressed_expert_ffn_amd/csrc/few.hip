@@ -4,8 +4,9 @@
 // touched groups' bases is read once, for all tokens together, and the rows
 // sit in the registers as the 16 rows of a 16x16x32 MFMA operand (two tiles
 // beyond 16 tokens).  What is left to save is launches and latency, so the
-// pass has three kernels, each cut into workgroups of 16 columns of output
-// whose 16 wavefronts split the depth of the product:
+// pass has three kernels, four or five for some shapes, cut into workgroups of
+// 16 columns of output (32 of a 4-bit base) whose 4 to 16 wavefronts split
+// the depth of the product:
 //   route  router scores; the last workgroup to finish them selects groups
 //          and experts for every token and lists the touched groups; beside
 //          it, u = x A for every expert where that is less than a launch
@@ -14,15 +15,16 @@
 //          z + u B, the activation, the gate weight, the sum over the
 //          group's experts, and partials of h A_down over the columns
 //   down   y = sum over the touched groups of hbar W2, plus the residual
-//          tail (sum of the partials) B_down, for 16 columns of y
+//          tail (sum of the partials, taken by a launch of its own before
+//          this one where they are many) B_down
 // The rows of the up and down products belong to tokens; a token that did
 // not choose a group has a zero row in the down product, so the sum over
 // groups is the accumulator's own and no combine pass is left.
 //
-// Everything between the kernels is held in 32 bits, or as two 16-bit parts
-// of a 32-bit number where it feeds a 16-bit MFMA (the hidden sums), and
-// residual codes multiply as integers with their scale applied to the sum:
-// y is rounded once.
+// Everything between the kernels is held in 32 bits, or, where it feeds a
+// 16-bit MFMA (the hidden sums), as two 16-bit parts of a 32-bit number or as
+// one of an eighth of the result's step (hidden_planes below), and residual
+// codes multiply as integers with their scale applied to the sum.
 #include "few.h"
 #include "kernels.h"
 #include "q4.h"
@@ -99,7 +101,7 @@ __device__ __forceinline__ uint16_t round_bits(float v) {
 }
 
 // Type and 16-bit parts the gate-weighted hidden sums (and V) are held in for
-// the down product.  An fp16 number is exact to 2^-12, a sixteenth of what a
+// the down product.  An fp16 number is exact to 2^-11, an eighth of what a
 // bf16 result is rounded by, so bf16 activations on fp16 MFMAs need one part;
 // where the result has the MFMAs' own precision the sums keep two, 22 or 16
 // bits, so that y is rounded once.  A 4-bit base takes either MFMA type, hence
@@ -594,11 +596,9 @@ __global__ __launch_bounds__(NT) void few_route_kernel(FewArgs a) {
   if (!alone) {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    if (threadIdx.x == 0) {
-      const int n = __hip_atomic_fetch_add(a.ticket, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      s.last = n == nsb - 1 ? 1 : 0;
-      if (s.last) __hip_atomic_store(a.ticket, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);  // for the next pass
-    }
+    // the ticket wraps to zero with the last one, ready for the next pass
+    if (threadIdx.x == 0)
+      s.last = atomicInc(reinterpret_cast<unsigned*>(a.ticket), nsb - 1) == static_cast<unsigned>(nsb - 1) ? 1 : 0;
     __syncthreads();
     if (!s.last) return;
     asm volatile("" ::: "memory");
@@ -934,7 +934,8 @@ __global__ __launch_bounds__(NWV * 64) void few_up_kernel(FewArgs a) {
           hv[x][r] = on ? J.wgt * h : 0.f;
         }
         if (on) {
-          const int row = div_small(J.slot, a.over_ke), at = __popc(members & ((1u << t) - 1)) * a.ke + (J.slot - row * a.ke);
+          const int row = div_small(J.slot, a.over_ke);
+          const int at = __popc(members & ((1u << t) - 1)) * a.ke + (J.slot - row * a.ke);
           *reinterpret_cast<f4v*>(hw + at * FT + 16 * x + 4 * q) = f4v{hv[x][0], hv[x][1], hv[x][2], hv[x][3]};
         }
         v = down_factor<TY, RS>(J.ad[x], hv[x], v);

@@ -85,7 +85,8 @@ extern "C" int moe_forward_few(moe_handle* h, const void* X, int32_t T, void* Y,
   if (!h) return fail(MOE_ERR_INVALID_ARG, "null handle");
   const moe_config& c = h->cfg;
   if (T < 0 || T > c.T_max) return fail(MOE_ERR_INVALID_ARG, "T=%d outside [0, T_max=%d]", T, c.T_max);
-  if (T > FEW_MAX_T) return fail(MOE_ERR_INVALID_ARG, "T=%d is more than the %d tokens of a few-token pass", T, FEW_MAX_T);
+  if (T > FEW_MAX_T)
+    return fail(MOE_ERR_INVALID_ARG, "T=%d is more than the %d tokens of a few-token pass", T, FEW_MAX_T);
   if (T == 0) return routing ? moe_route(h, X, 0, routing, stream) : MOE_OK;
   if (!X || !Y) return fail(MOE_ERR_INVALID_ARG, "null X or Y");
   if (X == Y) return fail(MOE_ERR_INVALID_ARG, "X and Y may not alias");
@@ -143,7 +144,6 @@ extern "C" int moe_forward_few(moe_handle* h, const void* X, int32_t T, void* Y,
   a.At_s = h->At_s;
   a.at_gs = h->at_gs;
   a.at_sgs = h->at_sgs;
-  a.NU = h->NU;
   a.U = s.U;
   // The input factors of every expert are read beside the selection while they
   // take no longer than it and the launch that reading the chosen ones' alone

@@ -202,16 +202,19 @@ int moe_forward_noalloc(moe_handle* h, const void* X, int32_t T, void* Y,
 
 /* The whole layer for a few tokens, 0 <= T <= min(T_max, 32): what
  * moe_forward computes, by kernels that stream the weights of the touched
- * groups once for all tokens, in three launches (four where the residual
- * input factors are so many that only the chosen experts' are read).  The
- * only forward pass of a layer with a 4-bit base.  X (on a 16-byte boundary)
- * and Y as moe_forward, routing too; the handle's device must be current.
- * Sums and everything between the kernels are held to FP32 accuracy and Y is
- * rounded once, so results differ from moe_forward's by the roundings that
- * one makes (hidden sums and rank products in 16 bits), and the choice of an
- * expert may differ where two scores agree to FP32 rounding.  A token's
- * result depends on X's other rows only through the order of its sums; equal
- * calls give equal bits.  For a 4-bit base, activations and gate-weighted
+ * groups once for all tokens, in three launches (one more where the residual
+ * input factors are so many that only the chosen experts' are read, and one
+ * more where the partial rank products are many).  The only forward pass of a
+ * layer with a 4-bit base.  X (on a 16-byte boundary) and Y as moe_forward,
+ * routing too; the handle's device must be current.  Sums are held in FP32.
+ * The gate-weighted hidden sums between the two products are handed on in the
+ * base's type, in fp16 for a 4-bit base: 16-bit types as two parts, with bf16
+ * activations on an fp16 or 4-bit base as one, whose step is an eighth of
+ * the result's; beyond that type's range y is not finite.  So results differ
+ * from moe_forward's by the roundings that one makes (hidden sums and rank
+ * products in 16 bits), and the choice of an expert may differ where two
+ * scores agree to FP32 rounding.  A token's result depends on X's other rows
+ * only through the order of its sums; equal calls give equal bits.  For a 4-bit base, activations and gate-weighted
  * hidden sums that are infinite or NaN give NaN rather than an infinity.
  * Enqueue only, and capturable, as moe_forward; one handle is not re-entrant
  * (this entry has a workspace of its own in the handle). */

@@ -312,14 +312,41 @@ def test_a_four_bit_base_runs_nowhere_else():
         lay.close()
 
 
+def test_rows_behind_the_last_token_stay():
+    import torch
+    w, layer, lay, X = make("swiglu", "f16", "f16", "int4_g32", 16, (4, 4), 2, 2, 11, 256, 192)
+    try:
+        buf = torch.full((32, 256), 42.0, dtype=X.dtype, device="cuda")
+        lay.forward_few(X, buf[:11])
+        assert (buf[11:] == 42.0).all()
+        check_y(buf[:11], O.forward(layer), "f16")
+    finally:
+        lay.close()
+
+
+def test_repeated_passes_on_one_handle_give_equal_bits():
+    """The selection's ticket returns to zero with every pass."""
+    import torch
+    w, layer, lay, X = make("swiglu", "f16", "f16", "int4_g32", 16, (16, 16), 2, 4, 16, 1024, 192)
+    try:
+        Y = lay.forward_few(X)
+        outs = [lay.forward_few(X if i % 2 == 0 else X[:1 + i].contiguous()) for i in range(15)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(outs[i], Y) for i in range(0, 15, 2))
+        check_y(Y, O.forward(layer), "f16")
+    finally:
+        lay.close()
+
+
 @pytest.mark.parametrize("case", [
+    ("swiglu", "f16", "f16", "int4_g32", 16, (16, 64), 2, 8, 32, 64, 64),
     ("swiglu", "f16", "f16", "int4_g32", 16, (8, 4), 2, 2, 9, 256, 320),
     ("gelu_tanh", "bf16", "int4_g32", "none", 0, (4, 1), 2, 1, 32, 128, 192),
     ("swiglu", "f32", "f32", "f32", 8, (4, 4), 1, 2, 3, 128, 64),
-], ids=["f16", "int4", "f32"])
+], ids=["many", "f16", "int4", "f32"])
 def test_graph_replays_follow_their_input(case):
     import torch
-    w, layer, lay, X0 = make(*case)
+    w, layer, lay, X0 = make(*case, bias=0.0)
     try:
         X, Y = X0.clone(), torch.empty_like(X0)
         s = torch.cuda.Stream()
