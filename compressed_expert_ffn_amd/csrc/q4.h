@@ -40,7 +40,7 @@
 
 namespace cefn {
 
-constexpr int Q4_FAST_ROWS = 32;  // rows (tokens) one launch takes
+constexpr int Q4_ROWS = 32;  // rows (tokens) one launch takes
 
 template <int TY> struct Q4Type;
 template <> struct Q4Type<DT_F16> {

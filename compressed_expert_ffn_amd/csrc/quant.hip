@@ -344,8 +344,8 @@ int validate_quant(const moe_quant_config* c) {
   if (c->group != 32 && c->group != 64 && c->group != 128)
     return fail(MOE_ERR_UNSUPPORTED, "group %d is not 32, 64 or 128", c->group);
   if (c->x_dtype == MOE_F32) return fail(MOE_ERR_UNSUPPORTED, "x_dtype must be F16 or BF16");
-  if (c->n_in > (1 << 24) || c->n_out > (1 << 24) || static_cast<int64_t>(c->n_in) * c->n_out > (1LL << 36))
-    return fail(MOE_ERR_UNSUPPORTED, "n_in, n_out <= 2^24 and n_in * n_out <= 2^36");
+  if (c->n_in > (1 << 24) || c->n_out > (1 << 24) || static_cast<int64_t>(c->n_in) * c->n_out > (1LL << 31))
+    return fail(MOE_ERR_UNSUPPORTED, "n_in, n_out <= 2^24 and n_in * n_out <= 2^31");
   return MOE_OK;
 }
 
@@ -470,11 +470,12 @@ int moe_quant_matvec(const moe_quant* h, const void* X, int64_t ldx, int32_t T, 
     return fail(MOE_ERR_INVALID_ARG, "X and Y must be aligned to their type");
   int dev = -1;
   if (hipGetDevice(&dev) != hipSuccess) return fail(MOE_ERR_HIP, "no HIP device");
-  if (dev != h->device) return fail(MOE_ERR_INVALID_ARG, "handle lives on device %d, device %d is current", h->device, dev);
+  if (dev != h->device)
+    return fail(MOE_ERR_INVALID_ARG, "handle lives on device %d, device %d is current", h->device, dev);
   const bool aligned = !(reinterpret_cast<uintptr_t>(X) & 15) && ldx % 8 == 0 && h->cfg.n_in % 8 == 0;
-  for (int32_t t = 0; t < T; t += Q4_FAST_ROWS) {
+  for (int32_t t = 0; t < T; t += Q4_ROWS) {
     MatvecArgs a{h->shape, h->words, h->scales, static_cast<const uint16_t*>(X) + t * ldx, ldx,
-                 T - t < Q4_FAST_ROWS ? T - t : Q4_FAST_ROWS, static_cast<uint16_t*>(Y) + t * ldy, ldy};
+                 T - t < Q4_ROWS ? T - t : Q4_ROWS, static_cast<uint16_t*>(Y) + t * ldy, ldy};
     const hipError_t e = h->cfg.x_dtype == MOE_F16
                              ? launch_mv<DT_F16>(a, aligned, static_cast<hipStream_t>(stream))
                              : launch_mv<DT_BF16>(a, aligned, static_cast<hipStream_t>(stream));
@@ -489,7 +490,8 @@ int moe_quant_read(const moe_quant* h, int8_t* q, uint16_t* scale) {
   const size_t ns = static_cast<size_t>((h->cfg.n_in + h->cfg.group - 1) / h->cfg.group) * h->cfg.n_out;
   int dev = -1;
   if (hipGetDevice(&dev) != hipSuccess) return fail(MOE_ERR_HIP, "no HIP device");
-  if (dev != h->device) return fail(MOE_ERR_INVALID_ARG, "handle lives on device %d, device %d is current", h->device, dev);
+  if (dev != h->device)
+    return fail(MOE_ERR_INVALID_ARG, "handle lives on device %d, device %d is current", h->device, dev);
   DeviceBuffers tmp;
   if (hipMalloc(&tmp.p[0], n) != hipSuccess || hipMalloc(&tmp.p[1], ns * 2) != hipSuccess) {
     (void)hipGetLastError();

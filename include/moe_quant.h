@@ -21,7 +21,7 @@
 extern "C" {
 #endif
 
-/* 1 <= n_in, n_out <= 2^24 and n_in * n_out <= 2^36; group 32, 64 or 128 (the
+/* 1 <= n_in, n_out <= 2^24 and n_in * n_out <= 2^31; group 32, 64 or 128 (the
  * last group of a column may be short); x_dtype MOE_F16 or MOE_BF16, the type
  * of X and Y. */
 typedef struct {

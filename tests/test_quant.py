@@ -30,7 +30,7 @@ BAD = [
     (dict(group=0), L.MOE_ERR_UNSUPPORTED, "group"),
     (dict(x_dtype="f32"), L.MOE_ERR_UNSUPPORTED, "F16 or BF16"),
     (dict(n_in=1 << 25), L.MOE_ERR_UNSUPPORTED, "2^24"),
-    (dict(n_in=1 << 20, n_out=1 << 20), L.MOE_ERR_UNSUPPORTED, "2^36"),
+    (dict(n_in=1 << 20, n_out=1 << 12), L.MOE_ERR_UNSUPPORTED, "2^31"),
     (dict(q=None), L.MOE_ERR_INVALID_ARG, "either"),
     (dict(values=Q.ctypes.data), L.MOE_ERR_INVALID_ARG, "either"),
     (dict(scale=None), L.MOE_ERR_INVALID_ARG, "scale"),
