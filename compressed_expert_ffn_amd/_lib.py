@@ -171,6 +171,8 @@ def _device_ptr(a, keep):
     if a is None:
         return None
     if isinstance(a, torch.Tensor):
+        if a.is_cuda and a.get_device() != torch.cuda.current_device():
+            raise ValueError(f"weights on {a.device}, but device {torch.cuda.current_device()} is current")
         t = a.contiguous() if a.is_cuda else a.contiguous().cuda()
         keep.append(t)
         return t.data_ptr()
@@ -461,6 +463,8 @@ class QuantLinear:
             if isinstance(a, torch.Tensor):
                 if a.is_cuda and not w.on_device:
                     raise ValueError("q, scale and values must all be on the device or all on the host")
+                if a.is_cuda and a.get_device() != torch.cuda.current_device():
+                    raise ValueError(f"{name} is on {a.device}, but device {torch.cuda.current_device()} is current")
                 a = a.contiguous()
                 kind = {torch.int8: "i8", torch.float16: "f16", torch.float32: "f32",
                         torch.bfloat16: "bf16"}.get(a.dtype)

@@ -262,3 +262,17 @@ def test_streams_and_graph_replays():
         torch.cuda.synchronize()
         assert torch.equal(Y, eager), rep
     lin.close()
+
+
+def test_weights_on_another_device_than_the_current_one_are_refused(monkeypatch):
+    import torch
+    from compressed_expert_ffn_amd import _lib as L
+    q = torch.zeros((64, 32), dtype=torch.int8, device="cuda")
+    scale = torch.ones((2, 32), dtype=torch.float16, device="cuda")
+    base = torch.zeros((2, 64, 64), dtype=torch.float16, device="cuda")
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    with pytest.raises(ValueError, match="current"):
+        L.QuantLinear(64, 32, 32, "f16", q=q, scale=scale)
+    cfg = L.make_config(4, 64, 64, 2, 1, 1, 1, 0, "gelu_tanh", "f16", "f16", "none")
+    with pytest.raises(ValueError, match="current"):
+        L.Layer(cfg, dict(W_grp=torch.zeros((64, 2), device="cuda"), base=[base, base]), on_device=True)
