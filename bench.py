@@ -231,13 +231,16 @@ def cpu_baseline(w, inputs, budget_s: float) -> dict:
 
 
 def side_modes(args, w, inputs) -> None:
-    """The backward pass, or the forward pass with offloaded groups: one
-    JSON line with the time per call (HIP events around the timed calls on
-    the launch stream) and the work rate."""
+    """The backward pass, the forward pass with offloaded groups, or the
+    few-token forward pass: one JSON line with the time per call (HIP events
+    around the timed calls on the launch stream) and the work rate."""
     import numpy as np
     import torch
     from compressed_expert_ffn_amd import _lib as L
     from compressed_expert_ffn_amd import synth
+    if args.mode == "few":
+        few_mode(args, w, inputs)
+        return
     lay = L.Layer(L.config_from_workload(w), inputs)
     Xh = inputs["X"]
     if w.x_dtype == "bf16":
@@ -296,6 +299,59 @@ def side_modes(args, w, inputs) -> None:
     print(json.dumps(out), flush=True)
 
 
+def few_mode(args, w, inputs) -> None:
+    """The first --tokens tokens through moe_forward_few, and through
+    moe_forward beside it (not for a 4-bit base), on two copies of the weights
+    in turn."""
+    import numpy as np
+    import torch
+    from compressed_expert_ffn_amd import _lib as L
+    from compressed_expert_ffn_amd import synth
+    T = args.tokens
+    base = w.base_dtype
+    if args.int4_base:
+        base = "int4_g32"
+        inputs = dict(inputs, base=[synth.storage_to_f64(b, w.base_dtype).astype(np.float32) for b in inputs["base"]])
+    cfg = L.make_config(T, w.d, w.f, w.G, w.K, w.top_groups, w.top_experts, w.r, w.act, w.x_dtype, base, w.resid)
+    lays = [L.Layer(cfg, inputs) for _ in range(2)]
+    Xh = inputs["X"][:T]
+    X = (torch.from_numpy(Xh.view(np.int16)).cuda().view(torch.bfloat16) if w.x_dtype == "bf16"
+         else torch.from_numpy(Xh).cuda())
+    Y = torch.empty_like(X)
+    st = torch.cuda.current_stream()
+
+    def timed(call):
+        for i in range(max(2, args.warmup)):
+            call(lays[i % 2])
+        torch.cuda.synchronize()
+        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        e0.record(st)
+        for i in range(args.steps):
+            call(lays[i % 2])
+        e1.record(st)
+        torch.cuda.synchronize()
+        return e0.elapsed_time(e1) / args.steps
+
+    ms = timed(lambda lay: lay.forward_few(X, Y))
+    bufs = lays[0].route_buffers(T)
+    lays[0].forward_few(X, Y, route_bufs=bufs)
+    tg = int((bufs["gcounts"] > 0).sum())
+    te = int((bufs["counts"] > 0).sum())
+    bb = {"f32": 4, "f16": 2, "bf16": 2, "int4_g32": 0.5 + 2 / 32}[base]
+    rb = resid_bytes_per_entry(w)
+    nbytes = (tg * sum(a * b for a, b in w.proj_dims()) * bb + te * w.r * sum(a + b for a, b in w.proj_dims()) * rb +
+              w.d * (w.G + (tg * w.K if w.K > 1 else 0)) * 4 + 2 * T * w.d * (4 if w.x_dtype == "f32" else 2))
+    out = dict(metric="few", workload=w.name, T=T, base=base, steps=args.steps, warmup=args.warmup,
+               ms_per_call=round(ms, 5), tokens_per_s=round(T / (ms * 1e-3), 1), touched_groups=tg, touched_experts=te,
+               gb_per_s=round(nbytes / (ms * 1e-3) / 1e9, 1),
+               note="bytes: weights of the touched groups and experts, router, X and Y, each once")
+    if base != "int4_g32":
+        out["moe_forward_ms_per_call"] = round(timed(lambda lay: lay.forward(X, Y)), 5)
+    for lay in lays:
+        lay.close()
+    print(json.dumps(out), flush=True)
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--gpus", type=int, default=1)
@@ -305,9 +361,11 @@ def main():
     ap.add_argument("--copies", type=int, default=0,
                     help="weight copies rotated between steps (0: 2 for the decode layer, else 1)")
     ap.add_argument("--no-graph", action="store_true", help="plain stream launches only")
-    ap.add_argument("--mode", choices=("forward", "backward", "offload"), default="forward",
+    ap.add_argument("--mode", choices=("forward", "backward", "offload", "few"), default="forward",
                     help="backward: time moe_backward; offload: moe_forward_offload with --slots device slots")
     ap.add_argument("--slots", type=int, default=0, help="offload mode: device group slots (0: G/2)")
+    ap.add_argument("--tokens", type=int, default=1, help="few mode: tokens per call (1 to 32)")
+    ap.add_argument("--int4-base", action="store_true", help="few mode: hold the base in 4 bits")
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--cpu-budget", type=float, default=20.0)
     ap.add_argument("--copy-calibration", action="store_true",
