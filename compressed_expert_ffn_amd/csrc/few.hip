@@ -17,14 +17,15 @@
 //   down   y = sum over the touched groups of hbar W2, plus the residual
 //          tail (sum of the partials, taken by a launch of its own before
 //          this one where they are many) B_down
-// The rows of the up and down products belong to tokens; a token that did
-// not choose a group has a zero row in the down product, so the sum over
-// groups is the accumulator's own and no combine pass is left.
+// The sum over a token's groups is made where the down product is (in the
+// accumulator or the workgroup's own memory), so no combine pass is left.
 //
 // Everything between the kernels is held in 32 bits, or, where it feeds a
 // 16-bit MFMA (the hidden sums), as two 16-bit parts of a 32-bit number or as
 // one of an eighth of the result's step (hidden_planes below), and residual
 // codes multiply as integers with their scale applied to the sum.
+#include <type_traits>
+
 #include "few.h"
 #include "kernels.h"
 #include "q4.h"
@@ -649,7 +650,7 @@ __global__ __launch_bounds__(NWV * 64) void few_up_kernel(FewArgs a) {
   constexpr int HT = hidden_type(TY, Q4);
   extern __shared__ __attribute__((aligned(16))) float red[];  // partial tiles, then the weighted h
   __shared__ __attribute__((aligned(16))) float z[2][MT * 16][20];  // 20: rows 16 bytes apart mod 128
-  __shared__ int srow[FEW_MAX_T];   // (token << 16) | row t*kg + rank, of the group's tokens
+  __shared__ int srow[FEW_MAX_T];   // rows t*kg + rank of the group's tokens
   const int Pin = a.Pin, FT = 32 / Pin, nfb = a.f / FT;
   const int ga = blockIdx.x / nfb, fb = blockIdx.x % nfb;
   if (ga >= a.glist[0]) return;
@@ -657,15 +658,22 @@ __global__ __launch_bounds__(NWV * 64) void few_up_kernel(FewArgs a) {
   const int g = rec.x, first = rec.y, ne = rec.z, n = rec.w;
   const int wave = wave_id(), lane = threadIdx.x & 63, l = lane & 15, q = lane >> 4;
   const int f0 = fb * FT;
-  // the group's tokens (bit t), their rows
+  // the group's tokens (bit t), their rows; the i-th of them is row i of the
+  // MFMA tiles, and rows past the last repeat it, which costs no further cache
+  // lines: a compute unit takes 2.5 cycles for each, and rows of all tokens are
+  // 16 an instruction (T = 32: 119 us a pass with them, 107 without; T = 16,
+  // fp16 base, 86.3 / 83.9)
   const int grow = lane < a.T ? a.grow[ga * FEW_MAX_T + lane] : -1;
   const uint32_t members = static_cast<uint32_t>(__ballot(grow >= 0));
-  if (wave == 0 && grow >= 0) srow[__popc(members & ((1u << lane) - 1))] = (lane << 16) | grow;
+  const int place = __popc(members & ((1u << (lane & 31)) - 1));
+  if (wave == 0 && grow >= 0) srow[place] = grow;
+  const int member = __builtin_amdgcn_ds_permute(4 * (grow >= 0 ? place : 63), lane);  // lane i: the i-th
   // The wavefront's jobs: a touched expert and up to 16 of its tokens, expert
   // first + wave, + NWV, ...  (beyond 16 tokens in the batch the expert's own
-  // are drawn together first, so few experts need a second job).  Their operands are few but cold, and behind a stream
-  // that fills the memory's queues a load takes microseconds: the first job's
-  // are read with the first weights, the next one's while a job runs.
+  // are drawn together first, so few experts need a second job).  Their
+  // operands are few but cold, and behind a stream that fills the memory's
+  // queues a load takes microseconds: the first job's are read with the first
+  // weights, the next one's while a job runs.
   struct Job {
     int slot;
     float wgt;
@@ -727,102 +735,112 @@ __global__ __launch_bounds__(NWV * 64) void few_up_kernel(FewArgs a) {
   const XE* xp[MT];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
-    xp[m] = static_cast<const XE*>(a.X) + static_cast<long>(min(16 * m + l, a.T - 1)) * a.d + 8 * q;
+    xp[m] = static_cast<const XE*>(a.X) + static_cast<long>(__shfl(member, min(16 * m + l, n - 1))) * a.d + 8 * q;
   f4v acc[2][MT];
 #pragma unroll
   for (int c = 0; c < 2; ++c)
 #pragma unroll
     for (int m = 0; m < MT; ++m) acc[c][m] = f4v{0.f, 0.f, 0.f, 0.f};
-  if constexpr (Q4) {
-    const uint32_t* wp =
-        static_cast<const uint32_t*>(a.W1) + g * a.w1_gs + (static_cast<long>(fb) * a.w1_units * 64 + lane) * 4;
-    const uint16_t* sp = a.W1_s + g * a.w1_sgs + (static_cast<long>(fb) * a.w1_units * 16 + l) * 4;
-    struct Slot {
-      Raw<XT> x[2][MT];
-      u4v w;
-      u2v s;
-    };
-    const B ones = q4_ones<TY>();
-    stream_units<MT == 1 ? 4 : 2, Slot>(
-        u1 - u0,
-        [&](int i, Slot& s) {
-          const long u = u0 + i;
-          s.w = *reinterpret_cast<const u4v*>(wp + u * 256);
-          s.s = load_scales<4>(sp + u * 64);
+  // M tiles of rows
+  auto stream = [&](auto tiles) {
+    constexpr int M = decltype(tiles)::value;
+    if constexpr (Q4) {
+      const uint32_t* wp =
+          static_cast<const uint32_t*>(a.W1) + g * a.w1_gs + (static_cast<long>(fb) * a.w1_units * 64 + lane) * 4;
+      const uint16_t* sp = a.W1_s + g * a.w1_sgs + (static_cast<long>(fb) * a.w1_units * 16 + l) * 4;
+      struct Slot {
+        Raw<XT> x[2][M];
+        u4v w;
+        u2v s;
+      };
+      const B ones = q4_ones<TY>();
+      stream_units<M == 1 ? 4 : 2, Slot>(
+          u1 - u0,
+          [&](int i, Slot& s) {
+            const long u = u0 + i;
+            s.w = *reinterpret_cast<const u4v*>(wp + u * 256);
+            s.s = load_scales<4>(sp + u * 64);
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int m = 0; m < MT; ++m) s.x[h][m] = load_raw<XT>(xp[m] + u * 64 + 32 * h);
-        },
-        [&](const Slot& s) {
+              for (int m = 0; m < M; ++m) s.x[h][m] = load_raw<XT>(xp[m] + u * 64 + 32 * h);
+          },
+          [&](const Slot& s) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            f4v off[MT];
-            B x[MT];
+            for (int h = 0; h < 2; ++h) {
+              f4v off[M];
+              B x[M];
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-              x[m] = raw_to_frag<XT, TY>(s.x[h][m]);
-              const f4v sum = mfma16<TY>(x[m], ones, f4v{0.f, 0.f, 0.f, 0.f});
+              for (int m = 0; m < M; ++m) {
+                x[m] = raw_to_frag<XT, TY>(s.x[h][m]);
+                const f4v sum = mfma16<TY>(x[m], ones, f4v{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
-              for (int i = 0; i < 4; ++i) off[m][i] = -kQ4Offset * sum[i];
-            }
+                for (int i = 0; i < 4; ++i) off[m][i] = -kQ4Offset * sum[i];
+              }
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const uint32_t word = s.w[2 * h + c];
-              const B b = q4_frag<TY>(word);
-              const float sc = scale_at(s.s, 2 * h + c);
+              for (int c = 0; c < 2; ++c) {
+                const uint32_t word = s.w[2 * h + c];
+                const B b = q4_frag<TY>(word);
+                const float sc = scale_at(s.s, 2 * h + c);
 #pragma unroll
-              for (int m = 0; m < MT; ++m) {
-                const f4v p = mfma16<TY>(x[m], b, off[m]);
+                for (int m = 0; m < M; ++m) {
+                  const f4v p = mfma16<TY>(x[m], b, off[m]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[c][m][i] += sc * p[i];
+                  for (int i = 0; i < 4; ++i) acc[c][m][i] += sc * p[i];
+                }
               }
             }
-          }
-        },
-        between);
+          },
+          between);
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
+      for (int c = 0; c < 2; ++c)
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+        for (int m = 0; m < M; ++m)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[c][m][i] *= Q4Type<TY>::undo;
-  } else {
-    constexpr int es = TY == DT_F32 ? 4 : 2;
-    const char* wp[2];
+          for (int i = 0; i < 4; ++i) acc[c][m][i] *= Q4Type<TY>::undo;
+    } else {
+      constexpr int es = TY == DT_F32 ? 4 : 2;
+      const char* wp[2];
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int n32 = Pin == 2 ? (fb & ~1) + c : fb, half = Pin == 2 ? fb & 1 : c;
-      wp[c] = static_cast<const char*>(a.W1) +
-              (g * a.w1_gs + ((static_cast<long>(n32) * (a.d / 16) + q) * 64 + 16 * half + l) * 8) * es;
-    }
-    struct Slot {
-      Raw<XT> x[2][MT];
-      B w[2][2];
-    };
-    stream_units<TY == DT_F32 ? 1 : MT == 1 ? 3 : 2, Slot>(
-        u1 - u0,
-        [&](int i, Slot& s) {
-          const long u = u0 + i;
+      for (int c = 0; c < 2; ++c) {
+        const int n32 = Pin == 2 ? (fb & ~1) + c : fb, half = Pin == 2 ? fb & 1 : c;
+        wp[c] = static_cast<const char*>(a.W1) +
+                (g * a.w1_gs + ((static_cast<long>(n32) * (a.d / 16) + q) * 64 + 16 * half + l) * 8) * es;
+      }
+      struct Slot {
+        Raw<XT> x[2][M];
+        B w[2][2];
+      };
+      stream_units<TY == DT_F32 ? 1 : M == 1 ? 3 : 2, Slot>(
+          u1 - u0,
+          [&](int i, Slot& s) {
+            const long u = u0 + i;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
+            for (int h = 0; h < 2; ++h) {
 #pragma unroll
-            for (int c = 0; c < 2; ++c) s.w[h][c] = load_frag<TY>(wp[c] + (u * 2048 + 256 * h) * es);
+              for (int c = 0; c < 2; ++c) s.w[h][c] = load_frag<TY>(wp[c] + (u * 2048 + 256 * h) * es);
 #pragma unroll
-            for (int m = 0; m < MT; ++m) s.x[h][m] = load_raw<XT>(xp[m] + u * 64 + 32 * h);
-          }
-        },
-        [&](const Slot& s) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-              const B x = raw_to_frag<XT, TY>(s.x[h][m]);
-#pragma unroll
-              for (int c = 0; c < 2; ++c) acc[c][m] = mfma16<TY>(x, s.w[h][c], acc[c][m]);
+              for (int m = 0; m < M; ++m) s.x[h][m] = load_raw<XT>(xp[m] + u * 64 + 32 * h);
             }
-        },
-        between);
+          },
+          [&](const Slot& s) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int m = 0; m < M; ++m) {
+                const B x = raw_to_frag<XT, TY>(s.x[h][m]);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) acc[c][m] = mfma16<TY>(x, s.w[h][c], acc[c][m]);
+              }
+          },
+          between);
+    }
+  };
+  if constexpr (MT == 2) {
+    if (n > 16) stream(std::integral_constant<int, 2>{});
+    else stream(std::integral_constant<int, 1>{});
+  } else {
+    stream(std::integral_constant<int, 1>{});
   }
 #pragma unroll
   for (int c = 0; c < 2; ++c)
@@ -830,7 +848,7 @@ __global__ __launch_bounds__(NWV * 64) void few_up_kernel(FewArgs a) {
     for (int m = 0; m < MT; ++m)
       *reinterpret_cast<f4v*>(red + ((wave * 2 + c) * MT + m) * 256 + lane * 4) = acc[c][m];
   __syncthreads();
-  for (int v = threadIdx.x; v < MT * 16 * 32; v += NWV * 64) {
+  for (int v = threadIdx.x; v < n * 32; v += NWV * 64) {
     const int row = v >> 5, col = v & 31;
     z[col >> 4][row][col & 15] = block_sum<NWV, 2, MT>(red, row, col);
   }
@@ -853,10 +871,10 @@ __global__ __launch_bounds__(NWV * 64) void few_up_kernel(FewArgs a) {
     // the group's experts are its base: one activation, their gates summed
     for (int v = threadIdx.x; v < n * FT; v += NWV * 64) {
       const int c = v % FT, i = v / FT;
-      const int t = srow[i] >> 16, row = srow[i] & 0xFFFF;
+      const int row = srow[i];
       float wgt = 0.f;
       for (int b = 0; b < a.ke; ++b) wgt += a.w[row * a.ke + b];
-      const float h = a.act == ACT_SWIGLU ? silu_f(z[0][t][c]) * z[1][t][c] : gelu_tanh_f(z[c >> 4][t][c & 15]);
+      const float h = a.act == ACT_SWIGLU ? silu_f(z[0][i][c]) * z[1][i][c] : gelu_tanh_f(z[c >> 4][i][c & 15]);
       store_hidden(row, c, wgt * h);
     }
   } else {
@@ -872,7 +890,7 @@ __global__ __launch_bounds__(NWV * 64) void few_up_kernel(FewArgs a) {
       const int e = je;
       const Job J = job;
       const bool on = J.slot >= 0;
-      const int t = on ? div_small(J.slot, a.over_k) : 0;
+      const int t = on ? div_small(J.slot, a.over_k) : 0, i = __popc(members & ((1u << t) - 1));
       // u, then the next job's operands behind it
       float u[2][8];
 #pragma unroll
@@ -919,7 +937,7 @@ __global__ __launch_bounds__(NWV * 64) void few_up_kernel(FewArgs a) {
           const u4v hi = __builtin_bit_cast(u4v, bu), lo = __builtin_bit_cast(u4v, round_frag<TY>(rest));
           bu = __builtin_bit_cast(B, part ? lo : hi);
         }
-        const f4v zz = mfma16<TY>(bw, bu, *reinterpret_cast<const f4v*>(&z[x][t][4 * q]));
+        const f4v zz = mfma16<TY>(bw, bu, *reinterpret_cast<const f4v*>(&z[x][i][4 * q]));
 #pragma unroll
         for (int r = 0; r < 4; ++r) hv[x][r] = zz[r];
       }
@@ -935,7 +953,7 @@ __global__ __launch_bounds__(NWV * 64) void few_up_kernel(FewArgs a) {
         }
         if (on) {
           const int row = div_small(J.slot, a.over_ke);
-          const int at = __popc(members & ((1u << t) - 1)) * a.ke + (J.slot - row * a.ke);
+          const int at = i * a.ke + (J.slot - row * a.ke);
           *reinterpret_cast<f4v*>(hw + at * FT + 16 * x + 4 * q) = f4v{hv[x][0], hv[x][1], hv[x][2], hv[x][3]};
         }
         v = down_factor<TY, RS>(J.ad[x], hv[x], v);
@@ -948,7 +966,7 @@ __global__ __launch_bounds__(NWV * 64) void few_up_kernel(FewArgs a) {
     }
     __syncthreads();
     for (int v = threadIdx.x; v < n * FT; v += NWV * 64) {
-      const int c = v % FT, i = v / FT, row = srow[i] & 0xFFFF;
+      const int c = v % FT, i = v / FT, row = srow[i];
       float s = 0.f;
       for (int b = 0; b < a.ke; ++b) s += hw[(i * a.ke + b) * FT + c];
       store_hidden(row, c, s);
@@ -980,60 +998,105 @@ __global__ __launch_bounds__(NT) void few_vsum_kernel(FewArgs a) {
 
 // ----------------------------------------------------------------- down --
 // grid: one workgroup per 16 columns of y.  Its wavefronts take consecutive
-// ranges of the touched groups' depths, laid end to end.  MFMA rows: with
-// 32-bit MFMAs token 16 m + r of tile m; with 16-bit ones the two parts of
-// the hidden sums are rows of their own: up to 8 tokens share one tile
-// (parts in rows 0-7 and 8-15), else tile m holds part m / (MT / 2) of
-// tokens 16 (m % (MT / 2)) + r.
+// ranges of the touched groups' depths, laid end to end.  One tile of MFMA
+// rows: 16 tokens, or 8 where the hidden sums have two parts, which are rows
+// of their own (parts in rows 0-7 and 8-15).
+//   MT = 1: the batch fits the tile.  Row r is token r in every group, a
+// token without the group reads a row of zeros, and the sum over groups is
+// the accumulator's own.
+//   MT > 1: a group's tokens are gathered into pieces of a tile's rows, most
+// often one, and a wavefront adds its sums to its own [T][16] block of LDS
+// where a piece ends.  Measured (us a pass, tiles of all tokens in every
+// group / pieces; d = 4096, f = 1536, 16 groups): T = 32 fp16 base 134 / 126,
+// 4-bit base 107 / 92, T = 9 fp16 70.1 / 71.2.
 //
 // The residual tail V B_down is more depth of the same product: two touched
 // experts' 16 rank columns are one 32-deep step, whose rows are the V of the
 // tokens that chose the expert (zero for the others).  A 4-bit factor's scale
 // varies along the rank columns, i.e. along the depth, so it multiplies V,
 // which then splits into two 16-bit parts like the hidden sums.
+__host__ __device__ inline int few_groups(const FewArgs& a) { return a.G < a.T * a.kg ? a.G : a.T * a.kg; }
+
 constexpr int kDownPartials = 16;  // partials of V a thread reads at a time
 constexpr int kDownBatches = 3;
 
 template <int XT, int TY, bool Q4, int RS, int MT>
 __global__ __launch_bounds__(NT) void few_down_kernel(FewArgs a) {
   using B = typename Frag<TY>::T;
-  extern __shared__ __attribute__((aligned(16))) float red[];  // [NW][MT][256], V and a zero row, partials, grow
+  // [NW][256] or [NW][T][16], V and a zero row, partials of V, grow, the pieces and their number
+  extern __shared__ __attribute__((aligned(16))) float red[];
   const int n = blockIdx.x, nv = RS != RS_NONE ? a.T * a.k * 16 : 0;
-  float* V = red + NW * MT * 256;
+  constexpr bool pieces = MT > 1;
+  constexpr int planes = hidden_planes(XT, TY);
+  constexpr int ROWS = 16 / planes;  // tokens of a tile
+  const int block = pieces ? a.T * 16 : 256;
+  float* V = red + NW * block;
   float* vpart = V + nv + 16;
   int16_t* grow = reinterpret_cast<int16_t*>(vpart + (nv && !a.v_sum ? NT : 0));
   const int ng = a.glist[0];
   const int tid = threadIdx.x, wave = wave_id(), lane = tid & 63, l = lane & 15, q = lane >> 4;
-  for (int i = tid; i < ng * (FEW_MAX_T / 2); i += NT)
-    reinterpret_cast<int*>(grow)[i] = reinterpret_cast<const int*>(a.grow)[i];
-  __syncthreads();
-  constexpr int planes = hidden_planes(XT, TY);
+  float* own = red + wave * block;
+  int* piece = reinterpret_cast<int*>(grow + few_groups(a) * FEW_MAX_T);  // (first token << 16) | group ordinal
+  int np = ng;
+  if constexpr (pieces) {
+    // a group's rows, absent ones behind them
+    for (int i = wave; i < ng; i += NW) {
+      const int row = lane < a.T ? a.grow[i * FEW_MAX_T + lane] : -1;
+      const unsigned long long m = __ballot(row >= 0), below = (1ull << lane) - 1;
+      const int at = row >= 0 ? __popcll(m & below) : __popcll(m) + __popcll(~m & below);
+      if (at < FEW_MAX_T) grow[i * FEW_MAX_T + at] = static_cast<int16_t>(row);
+    }
+    if (wave == NW - 1) {
+      int before = 0;
+      for (int i0 = 0; i0 < ng; i0 += 64) {
+        const int i = i0 + lane, count = i < ng ? (a.grec[i].w + ROWS - 1) / ROWS : 0;
+        int upto = count;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+          const int v = __shfl_up(upto, d);
+          upto += lane >= d ? v : 0;
+        }
+        for (int p = 0; p < count; ++p) piece[1 + before + upto - count + p] = (p * ROWS << 16) | i;
+        before += __shfl(upto, 63);
+      }
+      if (lane == 0) piece[0] = before;
+    }
+    for (int i = lane; i < block; i += 64) own[i] = 0.f;
+    __syncthreads();
+    np = __builtin_amdgcn_readfirstlane(piece[0]);
+  } else {
+    for (int i = tid; i < ng * (FEW_MAX_T / 2); i += NT)
+      reinterpret_cast<int*>(grow)[i] = reinterpret_cast<const int*>(a.grow)[i];
+    __syncthreads();
+  }
   constexpr int UNIT = Q4 ? 128 : 64, NS = UNIT / 32;
   constexpr bool packed = planes == 2 && MT == 1;
   constexpr int TM = planes == 1 ? MT : MT > 1 ? MT / 2 : 1;  // tiles of tokens
   const int nf = (a.f + UNIT - 1) / UNIT;
-  const int units = ng * nf;
+  const int units = np * nf;
   const int u0 = static_cast<int>(static_cast<long>(units) * wave / NW);
   const int u1 = static_cast<int>(static_cast<long>(units) * (wave + 1) / NW);
-  f4v acc[MT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) acc[m] = f4v{0.f, 0.f, 0.f, 0.f};
-  // the stream's place: group ordinal, unit inside it, the lane's rows
-  int at_i = 0, ga = u0 / nf, kb = u0 - ga * nf;
+  f4v acc = {0.f, 0.f, 0.f, 0.f};
+  // the stream's place: piece (a group where the batch fits the tile), unit inside it, the lane's row
+  int at_i = 0, pi = u0 / nf, kb = u0 - pi * nf;
   using HE = typename Elem<TY>::T;
-  const HE* hp[MT];
+  const HE* hp = nullptr;
   const char* wp = nullptr;
   const uint16_t* sp = nullptr;
   constexpr int es = TY == DT_F32 ? 4 : 2;
   auto enter = [&]() {
-    const int g = a.grec[ga].x;
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const int t = packed ? (l & 7) : 16 * (m % TM) + l, plane = packed ? l >> 3 : m / TM;
-      const int row = t < a.T ? grow[ga * FEW_MAX_T + t] : -1;
-      // a token that did not choose the group reads the row of zeros
-      hp[m] = static_cast<const HE*>(a.H) + (static_cast<long>(row < 0 ? a.zero_row : row) * planes + plane) * a.f;
+    int ga = pi, row;
+    const int r = l & (ROWS - 1), plane = l / ROWS;
+    if constexpr (pieces) {
+      const int p = __builtin_amdgcn_readfirstlane(piece[1 + pi]);
+      ga = p & 0xFFFF;
+      row = grow[ga * FEW_MAX_T + (p >> 16) + r];
+    } else {
+      row = r < a.T ? grow[ga * FEW_MAX_T + r] : -1;
     }
+    const int g = a.grec[ga].x;
+    // a token that did not choose the group, a row past a piece's last: zeros
+    hp = static_cast<const HE*>(a.H) + (static_cast<long>(row < 0 ? a.zero_row : row) * planes + plane) * a.f;
     if constexpr (Q4) {
       wp = reinterpret_cast<const char*>(static_cast<const uint32_t*>(a.W2) + g * a.w2_gs +
                                          (static_cast<long>(n) * nf * 64 + lane) * 4);
@@ -1049,8 +1112,31 @@ __global__ __launch_bounds__(NT) void few_down_kernel(FewArgs a) {
     at_i = i;
     if (++kb == nf) {
       kb = 0;
-      ++ga;
+      ++pi;
       enter();
+    }
+  };
+  // a piece's sums to its tokens' rows of the wavefront's block; cur: piece of the sums
+  int cur = pi;
+  auto leave = [&]() {
+    const int p = __builtin_amdgcn_readfirstlane(piece[1 + cur]);
+    const int16_t* rows = grow + (p & 0xFFFF) * FEW_MAX_T + (p >> 16);
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      float s = Q4 ? acc[v] * Q4Type<TY == DT_F32 ? DT_F16 : TY>::undo : acc[v];
+      if constexpr (planes == 2) s += __shfl_xor(s, 32);
+      const int row = rows[(4 * q + v) & (ROWS - 1)];
+      if (4 * q + v < ROWS && row >= 0) own[div_small(row, a.over_kg) * 16 + l] += s;
+      acc[v] = 0.f;
+    }
+    __builtin_amdgcn_wave_barrier();  // the next piece's lanes read what these wrote
+  };
+  auto follow = [&](int at) {
+    if constexpr (pieces) {
+      if (at != cur) {
+        leave();
+        cur = at;
+      }
     }
   };
   // the residual tail: steps of two touched experts, dealt to the wavefronts;
@@ -1089,6 +1175,9 @@ __global__ __launch_bounds__(NT) void few_down_kernel(FewArgs a) {
   };
   if constexpr (RS != RS_NONE)
     if (wave < steps) tail_find(wave);
+  f4v tacc[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) tacc[m] = f4v{0.f, 0.f, 0.f, 0.f};
   auto tail_use = [&](const Tail& tail) {
     B b;
     if constexpr (TY == DT_F32) {
@@ -1116,17 +1205,17 @@ __global__ __launch_bounds__(NT) void few_down_kernel(FewArgs a) {
       }
       const B hi = round_frag<TY>(v);
       if constexpr (planes == 1) {
-        acc[m] = mfma16<TY>(hi, b, acc[m]);
+        tacc[m] = mfma16<TY>(hi, b, tacc[m]);
       } else {
 #pragma unroll
         for (int r = 0; r < 8; ++r) rest[r] = v[r] - static_cast<float>(hi[r]);
         const B lo = round_frag<TY>(rest);
         if constexpr (packed) {
           const u4v x = __builtin_bit_cast(u4v, hi), y = __builtin_bit_cast(u4v, lo);
-          acc[0] = mfma16<TY>(__builtin_bit_cast(B, l < 8 ? x : y), b, acc[0]);
+          tacc[0] = mfma16<TY>(__builtin_bit_cast(B, l < 8 ? x : y), b, tacc[0]);
         } else {
-          acc[m] = mfma16<TY>(hi, b, acc[m]);
-          acc[TM + m] = mfma16<TY>(lo, b, acc[TM + m]);
+          tacc[m] = mfma16<TY>(hi, b, tacc[m]);
+          tacc[TM + m] = mfma16<TY>(lo, b, tacc[TM + m]);
         }
       }
     }
@@ -1164,70 +1253,69 @@ __global__ __launch_bounds__(NT) void few_down_kernel(FewArgs a) {
   };
   if constexpr (Q4) {
     struct Slot {
-      Raw<TY> x[NS][MT];
+      Raw<TY> x[NS];
       u4v w;
       u2v s;
+      int at;
     };
     const B ones = q4_ones<TY>();
-    stream_units<MT == 1 ? 2 : 1, Slot>(
+    stream_units<2, Slot>(
         u1 - u0,
         [&](int i, Slot& s) {
           seek(i);
+          s.at = pi;
           s.w = *reinterpret_cast<const u4v*>(wp + static_cast<long>(kb) * 1024);
           s.s = load_scales<4>(sp + static_cast<long>(kb) * 64);
 #pragma unroll
           for (int st = 0; st < NS; ++st) {
             // depths past f repeat the row's last ones (their codes are zero)
             const int k = min(kb * UNIT + 32 * st + 8 * q, a.f - 8);
-#pragma unroll
-            for (int m = 0; m < MT; ++m) s.x[st][m] = load_raw<TY>(hp[m] + k);
+            s.x[st] = load_raw<TY>(hp + k);
           }
         },
         [&](const Slot& s) {
+          follow(s.at);
 #pragma unroll
           for (int st = 0; st < NS; ++st) {
             const uint32_t word = s.w[st];
             const B b = q4_frag<TY>(word);
             const float sc = scale_at(s.s, st);
+            const B x = raw_to_frag<TY, TY>(s.x[st]);
+            const f4v sum = mfma16<TY>(x, ones, f4v{0.f, 0.f, 0.f, 0.f});
+            f4v off;
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-              const B x = raw_to_frag<TY, TY>(s.x[st][m]);
-              const f4v sum = mfma16<TY>(x, ones, f4v{0.f, 0.f, 0.f, 0.f});
-              f4v off;
+            for (int i = 0; i < 4; ++i) off[i] = -kQ4Offset * sum[i];
+            const f4v p = mfma16<TY>(x, b, off);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) off[i] = -kQ4Offset * sum[i];
-              const f4v p = mfma16<TY>(x, b, off);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) acc[m][i] += sc * p[i];
-            }
+            for (int i = 0; i < 4; ++i) acc[i] += sc * p[i];
           }
         },
         between);
+    if constexpr (!pieces) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[m][i] *= Q4Type<TY>::undo;
+      for (int i = 0; i < 4; ++i) acc[i] *= Q4Type<TY>::undo;
+    }
   } else {
     struct Slot {
-      Raw<TY> x[2][MT];
+      Raw<TY> x[2];
       B w[2];
+      int at;
     };
-    stream_units<TY == DT_F32 ? 2 : MT == 1 ? 4 : MT == 2 ? 3 : 2, Slot>(
+    stream_units<TY == DT_F32 ? 2 : 4, Slot>(
         u1 - u0,
         [&](int i, Slot& s) {
           seek(i);
+          s.at = pi;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             s.w[h] = load_frag<TY>(wp + (static_cast<long>(kb) * 2048 + 256 * h) * es);
-#pragma unroll
-            for (int m = 0; m < MT; ++m) s.x[h][m] = load_raw<TY>(hp[m] + kb * 64 + 32 * h + 8 * q);
+            s.x[h] = load_raw<TY>(hp + kb * 64 + 32 * h + 8 * q);
           }
         },
         [&](const Slot& s) {
+          follow(s.at);
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int m = 0; m < MT; ++m) acc[m] = mfma16<TY>(raw_to_frag<TY, TY>(s.x[h][m]), s.w[h], acc[m]);
+          for (int h = 0; h < 2; ++h) acc = mfma16<TY>(raw_to_frag<TY, TY>(s.x[h]), s.w[h], acc);
         },
         between);
   }
@@ -1242,15 +1330,36 @@ __global__ __launch_bounds__(NT) void few_down_kernel(FewArgs a) {
       tail_use(now);
     }
   }
+  if constexpr (pieces) {
+    if (u0 < u1) leave();
+    if constexpr (RS != RS_NONE) {
+      if (wave < steps) {
 #pragma unroll
-  for (int m = 0; m < MT; ++m) *reinterpret_cast<f4v*>(red + (wave * MT + m) * 256 + lane * 4) = acc[m];
+        for (int m = 0; m < TM; ++m)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const int t = 16 * m + 4 * q + v;
+            float s = tacc[m][v];
+            if constexpr (planes == 2) s += tacc[TM + m][v];
+            if (t < a.T) own[t * 16 + l] += s;
+          }
+      }
+    }
+  } else {
+    *reinterpret_cast<f4v*>(own + lane * 4) = acc + tacc[0];
+  }
   __syncthreads();
   for (int v = tid; v < a.T * 16; v += NT) {
     const int t = v >> 4, c = v & 15;
     float s = 0.f;
+    if constexpr (pieces) {
 #pragma unroll
-    for (int p = planes - 1; p >= 0; --p)  // the rests first
-      s += block_sum<NW, 1, MT>(red, packed ? t + 8 * p : 16 * TM * p + t, c);
+      for (int w = 0; w < NW; ++w) s += red[w * block + v];
+    } else {
+#pragma unroll
+      for (int p = planes - 1; p >= 0; --p)  // the rests first
+        s += block_sum<NW, 1, 1>(red, t + 8 * p, c);
+    }
     static_cast<typename Elem<XT>::T*>(a.Y)[static_cast<long>(t) * a.d + n * 16 + c] = from_f32<XT>(s);
   }
 }
@@ -1328,7 +1437,6 @@ hipError_t up_mt(const FewArgs& a, hipStream_t st) {
 template <int XT, int TY, bool Q4, int RS>
 hipError_t down_rs(const FewArgs& a, hipStream_t st) {
   const unsigned grid = a.d / 16;
-  const int groups = a.G < a.T * a.kg ? a.G : a.T * a.kg;
   const int nv = RS != RS_NONE ? a.T * a.k * 16 : 0;
   if (nv && a.v_sum) {
     hipLaunchKernelGGL(few_vsum_kernel, dim3((nv + 63) / 64), dim3(NT), 0, st, a);
@@ -1337,8 +1445,12 @@ hipError_t down_rs(const FewArgs& a, hipStream_t st) {
   }
   constexpr int planes = hidden_planes(XT, TY);
   const int mt = planes == 1 ? (a.T <= 16 ? 1 : 2) : a.T <= 8 ? 1 : a.T <= 16 ? 2 : 4;
-  const size_t lds = sizeof(float) * (static_cast<size_t>(NW) * mt * 256 + nv + 16 + (nv && !a.v_sum ? NT : 0)) +
-                     sizeof(int16_t) * groups * FEW_MAX_T;
+  // pieces: a group's are one more than its full tiles of tokens at most
+  const size_t tables = few_groups(a) * FEW_MAX_T * sizeof(int16_t) +
+                        (mt > 1 ? sizeof(int) * (1 + few_groups(a) + a.T * a.kg * planes / 16) : 0);
+  const size_t lds =
+      sizeof(float) * (static_cast<size_t>(NW) * (mt > 1 ? a.T * 16 : 256) + nv + 16 + (nv && !a.v_sum ? NT : 0)) +
+      tables;
   if (mt == 1) return go(few_down_kernel<XT, TY, Q4, RS, 1>, grid, NT, lds, a, st);
   if (mt == 2) return go(few_down_kernel<XT, TY, Q4, RS, 2>, grid, NT, lds, a, st);
   if constexpr (planes == 2) return go(few_down_kernel<XT, TY, Q4, RS, 4>, grid, NT, lds, a, st);
