@@ -376,7 +376,8 @@ __device__ void u_block(const FewArgs& a, int g, int nb, bool real, float* red) 
 struct SelectLds {
   int idx[FEW_MAX_T * MAX_SLOTS], gid[FEW_MAX_T * MAX_KG];
   float pg[FEW_MAX_T * MAX_KG];
-  int count[2][1024], pos[2][1024];  // tokens per group and per expert; non-empty bins before each
+  uint32_t mask[2][1024];  // tokens of each group and of each expert
+  int pos[2][1024];        // non-empty bins before each; then entries before each
   int wsum[2][NW];
   int last;
 };
@@ -455,27 +456,61 @@ __device__ __forceinline__ void select_tokens(const FewArgs& a, int t0, int nt, 
   }
 }
 
-// The caller's lists: an entry's place in its bin's list is the entries of
-// lower bins and those before it in its own (tokens ascend within a bin).
-__device__ __noinline__ void caller_lists(const int* bins, int n, int nbins, int per, int* counts, int* offsets,
-                                          int* perm) {
+// The tokens of each group and of each expert.
+__device__ __forceinline__ void make_masks(const FewArgs& a, SelectLds& s) {
   const int tid = threadIdx.x;
-#pragma unroll 1
-  for (int b = tid; b <= nbins; b += NT) {
-    int below = 0, mine = 0;
-#pragma unroll 1
-    for (int i = 0; i < n; ++i) {
-      below += bins[i] < b ? 1 : 0;
-      mine += bins[i] == b ? 1 : 0;
+  s.mask[0][tid] = 0;
+  s.mask[1][tid] = 0;
+  __syncthreads();
+  if (tid < a.T * a.kg) atomicOr(&s.mask[0][s.gid[tid]], 1u << div_small(tid, a.over_kg));
+  if (tid < a.T * a.k) atomicOr(&s.mask[1][s.idx[tid]], 1u << div_small(tid, a.over_k));
+  __syncthreads();
+}
+
+// The caller's lists, from the masks: an entry's place in its bin's list is
+// the entries of lower bins and those of lower tokens in its own.  (Counting
+// both by a loop over all entries took 7 us of a launch at T = 32, 8 experts
+// each.)
+__device__ __forceinline__ void caller_lists(const FewArgs& a, SelectLds& s) {
+  const int tid = threadIdx.x, wave = wave_id(), lane = tid & 63;
+  __syncthreads();  // pos is free
+  int upto[2], total[2];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    upto[x] = __popc(s.mask[x][tid]);
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int v = __shfl_up(upto[x], d);
+      upto[x] += lane >= d ? v : 0;
     }
-    if (counts && b < nbins) counts[b] = mine;
-    if (offsets) offsets[b] = below;
+    if (lane == 63) s.wsum[x][wave] = upto[x];
   }
-  if (perm && tid < n) {
-    int at = 0;
-#pragma unroll 1
-    for (int i = 0; i < n; ++i) at += (bins[i] < bins[tid] || (bins[i] == bins[tid] && i < tid)) ? 1 : 0;
-    perm[at] = tid / per;
+  __syncthreads();
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    int before = 0;
+    total[x] = 0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      const int c = s.wsum[x][w];
+      before += w < wave ? c : 0;
+      total[x] += c;
+    }
+    const int mine = __popc(s.mask[x][tid]), off = before + upto[x] - mine, bins = x ? a.E : a.G;
+    s.pos[x][tid] = off;
+    int* counts = x ? a.counts : a.gcounts;
+    int* offsets = x ? a.offsets : a.goffsets;
+    if (counts && tid < bins) counts[tid] = mine;
+    if (offsets && tid < bins) offsets[tid] = off;
+    if (offsets && tid == 0) offsets[bins] = total[x];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    int* perm = x ? a.perm : a.gperm;
+    if (!perm || tid >= a.T * (x ? a.k : a.kg)) continue;
+    const int b = x ? s.idx[tid] : s.gid[tid], t = div_small(tid, x ? a.over_k : a.over_kg);
+    perm[s.pos[x][b] + __popc(s.mask[x][b] & ((1u << t) - 1))] = t;
   }
 }
 
@@ -501,14 +536,8 @@ __device__ __forceinline__ void make_lists(const FewArgs& a, SelectLds& s, int16
     }
     return;
   }
-  // groups and experts side by side: tokens per bin, non-empty bins before each
-  s.count[0][tid] = 0;
-  s.count[1][tid] = 0;
-  __syncthreads();
-  if (tid < ng) atomicAdd(&s.count[0][s.gid[tid]], 1);
-  if (tid < na) atomicAdd(&s.count[1][s.idx[tid]], 1);
-  __syncthreads();
-  const unsigned long long m0 = __ballot(s.count[0][tid] > 0), m1 = __ballot(s.count[1][tid] > 0);
+  // groups and experts side by side: non-empty bins before each
+  const unsigned long long m0 = __ballot(s.mask[0][tid] != 0), m1 = __ballot(s.mask[1][tid] != 0);
   if (lane == 0) {
     s.wsum[0][wave] = __popcll(m0);
     s.wsum[1][wave] = __popcll(m1);
@@ -543,12 +572,12 @@ __device__ __forceinline__ void make_lists(const FewArgs& a, SelectLds& s, int16
     reinterpret_cast<int*>(a.grow)[i] = reinterpret_cast<const int*>(tab)[i];
   for (int i = tid; i < te * (FEW_MAX_T / 2); i += NT)
     reinterpret_cast<int*>(a.eslot)[i] = reinterpret_cast<const int*>(etab)[i];
-  if (resid && s.count[1][tid] > 0) a.elist[1 + s.pos[1][tid]] = tid;
-  if (tid < a.G && s.count[0][tid] > 0) {
+  if (resid && s.mask[1][tid]) a.elist[1 + s.pos[1][tid]] = tid;
+  if (tid < a.G && s.mask[0][tid]) {
     // an expert past the last has all touched ones before it
     const int first = resid ? s.pos[1][tid * a.K] : 0;
     const int end = !resid ? 0 : (tid + 1) * a.K < 1024 ? s.pos[1][(tid + 1) * a.K] : te;
-    a.grec[s.pos[0][tid]] = int4{tid, first, end - first, s.count[0][tid]};
+    a.grec[s.pos[0][tid]] = int4{tid, first, end - first, __popc(s.mask[0][tid])};
   }
 }
 
@@ -612,11 +641,9 @@ __global__ __launch_bounds__(NT) void few_route_kernel(FewArgs a) {
     __syncthreads();
     select_tokens(a, t0, nt, NC, sc, s);
   }
+  if (a.T > 1 || a.wants_lists) make_masks(a, s);
   make_lists(a, s, reinterpret_cast<int16_t*>(red));
-  if (a.wants_lists) {
-    caller_lists(s.gid, a.T * a.kg, a.G, a.kg, a.gcounts, a.goffsets, a.gperm);
-    caller_lists(s.idx, a.T * a.k, a.E, a.k, a.counts, a.offsets, a.perm);
-  }
+  if (a.wants_lists) caller_lists(a, s);
 }
 
 // U of the chosen experts only: one workgroup per two blocks of 32 factor
