@@ -411,37 +411,86 @@ __device__ __forceinline__ void gather_scores(const FewArgs& a, int t0, int nt, 
   }
 }
 
-// Selection for tokens t0 .. t0 + nt - 1 by one workgroup, a wavefront per
-// token for the groups and then per (token, chosen group) for the experts:
-// larger score first, ties to the lower index; gates are the softmax over the
-// chosen groups times the softmax over the chosen experts of each.
+// Top-k of up to 16 candidates by each row of 16 lanes (four jobs a
+// wavefront): the row's lane r ends up with selection r's exp(score - the
+// first's) and index, every lane with the sum of the k, added in order.
+__device__ __forceinline__ void row_topk(const float* sv, int n, int k, int lane, float& mye, int& myi, float& sum) {
+  const int c = lane & 15, shift = lane & 16;
+  float v = c < n ? sv[c] : -INFINITY;
+  v = (v == v) ? v : -INFINITY;
+  bool left = c < n;
+  float top = 0.f;
+  sum = 0.f;
+  mye = 0.f;
+  myi = -1;
+  auto turn = [](float x, auto ctrl) {  // the larger of x and the row's x that many lanes on
+    return fmaxf(x, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), decltype(ctrl)::value, 0xf, 0xf,
+                                                               false)));
+  };
+  using std::integral_constant;
+#pragma unroll 1
+  for (int r = 0; r < k; ++r) {
+    float best = left ? v : -INFINITY;
+    best = turn(best, integral_constant<int, 0x128>{});  // row_ror:8, 4, 2, 1
+    best = turn(best, integral_constant<int, 0x124>{});
+    best = turn(best, integral_constant<int, 0x122>{});
+    best = turn(best, integral_constant<int, 0x121>{});
+    const unsigned long long m = __ballot(left && v == best);
+    const uint32_t mine = (lane < 32 ? static_cast<uint32_t>(m) : static_cast<uint32_t>(m >> 32)) >> shift;
+    const int at = __ffs(static_cast<int>(mine & 0xFFFFu)) - 1;
+    if (c == at) left = false;
+    if (r == 0) top = best;
+    const float e = expf(best - top);
+    sum += e;
+    if (c == r) {
+      mye = e;
+      myi = at;
+    }
+  }
+}
+
+// Selection for tokens t0 .. t0 + nt - 1 by one workgroup, a job per token for
+// the groups and then per (token, chosen group) for the experts: larger score
+// first, ties to the lower index; gates are the softmax over the chosen groups
+// times the softmax over the chosen experts of each.  Up to 16 candidates are
+// a row of lanes each: four wavefronts share the issue of a SIMD, so what
+// counts is instructions (T = 32, 16 groups of 16: 9.1 us with a wavefront a
+// job, 3.1 with a row).
 __device__ __forceinline__ void select_tokens(const FewArgs& a, int t0, int nt, int NC, const float* sc, SelectLds& s) {
   const int wave = wave_id(), lane = threadIdx.x & 63;
 #pragma unroll 1
   for (int level = 0; level < (a.K > 1 ? 2 : 1); ++level) {
     const int n = level ? a.K : a.G, k = level ? a.ke : a.kg, jobs = level ? nt * a.kg : nt;
+    const int per = n <= 16 ? 4 : 1;  // jobs a wavefront takes at a time
 #pragma unroll 1
-    for (int i = wave; i < jobs; i += NW) {
+    for (int i0 = wave * per; i0 < jobs; i0 += NW * per) {
+      const int i = n <= 16 ? min(i0 + (lane >> 4), jobs - 1) : i0;
+      const int r = n <= 16 ? lane & 15 : lane;  // the lane's selection
       const int tok = level ? div_small(i, a.over_kg) : i;
       const int tr = t0 * a.kg + i;  // level 1: token * kg + rank
       const float* from = sc + tok * NC + (level ? a.G + s.gid[tr] * a.K : 0);
-      float v;
+      float e, sum = 0.f;
       int j;
-      wave_topk(from, n, k, lane, v, j);
-      const float e = lane < k ? expf(v - lane_value(v, 0)) : 0.f;
-      float sum = 0.f;
+      if (n <= 16) {
+        row_topk(from, n, k, lane, e, j, sum);
+        if (i0 + (lane >> 4) >= jobs) continue;
+      } else {
+        float v;
+        wave_topk(from, n, k, lane, v, j);
+        e = lane < k ? expf(v - lane_value(v, 0)) : 0.f;
 #pragma unroll 1
-      for (int r = 0; r < k; ++r) sum += lane_value(e, r);
+        for (int x = 0; x < k; ++x) sum += lane_value(e, x);
+      }
       const float p = e / sum;
-      if (lane >= k) continue;
+      if (r >= k) continue;
       int at, id = j;
       float w = p;
       if (level) {
-        at = tr * a.ke + lane;  // (t * kg + rank) * ke + b
+        at = tr * a.ke + r;  // (t * kg + rank) * ke + b
         id += s.gid[tr] * a.K;
         w *= s.pg[tr];
       } else {
-        at = (t0 + i) * a.kg + lane;
+        at = (t0 + i) * a.kg + r;
         s.gid[at] = j;
         s.pg[at] = p;
         a.gidx[at] = j;
