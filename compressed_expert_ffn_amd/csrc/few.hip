@@ -232,11 +232,15 @@ __device__ __forceinline__ float block_sum(const float* red, int row, int col) {
 // 4-bit factors: a 64-deep unit of the block is 256 words, word 64 q' + 32 h +
 // c for depths 64 u + 32 h + 8 q' .. and column c.  Lane 16 q + l takes words
 // 4 (16 q + l) .. + 3 in one load: columns 4 (l % 8) + i at half h = l / 8,
-// so the 16 columns of an MFMA are 8 real ones at both halves of the depth.
-// Each word multiplies the activations of both halves and the lane keeps its
-// own; two MFMAs for one, but a fourth of the loads (4-byte loads of each
-// half's 16 columns took 6.4 us of a 256-expert layer's launch).
-template <int XT, int TY, bool INT4, int MT>
+// so the 16 columns of an MFMA are 8 real ones at both halves of the depth,
+// and its 16 rows 8 tokens at both: the quarters of the product whose halves
+// agree are kept, two MFMAs for one, but a fourth of the weights' loads (4-byte
+// loads of each half's 16 columns took 6.4 us of a 256-expert layer's launch),
+// and a load of activations takes 8 whole cache lines (a pass
+// with rows of 16 tokens at one half each: 33.3 us, now 31.6, at T = 1, 124.4
+// and 124.1 at T = 32).  The next 8 tokens take the halves in the other order,
+// so the two quarters they keep are the ones that the first 8 leave.
+template <int XT, int TY, bool INT4, int T8>
 __device__ void u_block(const FewArgs& a, int g, int nb, bool real, float* red) {
   using XE = typename Elem<XT>::T;
   using B = typename Frag<TY>::T;
@@ -244,23 +248,26 @@ __device__ void u_block(const FewArgs& a, int g, int nb, bool real, float* red) 
   const int n64 = real ? a.d / 64 : 0, tid = threadIdx.x % (UW * 64);
   const int u0 = n64 * wave / UW, u1 = n64 * (wave + 1) / UW;
   const int cols = a.K * a.Pin * 16;  // column (j * Pin + p) * 16 + rho of the group
-  const XE* xp[MT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-    xp[m] = static_cast<const XE*>(a.X) + static_cast<long>(min(16 * m + l, a.T - 1)) * a.d + 8 * q;
   if constexpr (INT4) {
     const int h = l >> 3;
     const uint32_t* wp =
         static_cast<const uint32_t*>(a.At) + g * a.at_gs + static_cast<long>(nb) * (a.d / 16) * 64 + 4 * lane;
     const uint16_t* sp =
         a.At_s + g * a.at_sgs + (static_cast<long>(nb) * (a.d / 32) + h) * 32 + 4 * (l & 7);
+    constexpr int MT = (T8 + 1) / 2;  // tiles of 16 tokens
+    const bool first = (q >> 1) == h;  // the lane's quarter belongs to the first 8 tokens of a tile
+    const XE* xh[T8];
+#pragma unroll
+    for (int m = 0; m < T8; ++m)
+      xh[m] = static_cast<const XE*>(a.X) + static_cast<long>(min(8 * m + (l & 7), a.T - 1)) * a.d +
+              32 * (h ^ (m & 1)) + 8 * q;
     f4v acc[4][MT];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int m = 0; m < MT; ++m) acc[i][m] = f4v{0.f, 0.f, 0.f, 0.f};
     struct Slot {
-      Raw<XT> x[2][MT];
+      Raw<XT> x[T8];
       u4v w;
       u2v s;
     };
@@ -272,22 +279,18 @@ __device__ void u_block(const FewArgs& a, int g, int nb, bool real, float* red) 
           s.w = *reinterpret_cast<const u4v*>(wp + u * 256);
           s.s = load_scales<4>(sp + u * 64);
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh)
-#pragma unroll
-            for (int m = 0; m < MT; ++m) s.x[hh][m] = load_raw<XT>(xp[m] + u * 64 + 32 * hh);
+          for (int m = 0; m < T8; ++m) s.x[m] = load_raw<XT>(xh[m] + u * 64);
         },
         [&](const Slot& s) {
-          B x[2][MT];
-          f4v off[2][MT];
+          B x[T8];
+          f4v off[T8];
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh)
+          for (int m = 0; m < T8; ++m) {
+            x[m] = raw_to_frag<XT, TY>(s.x[m]);
+            const f4v sum = mfma16<TY>(x[m], ones, f4v{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-              x[hh][m] = raw_to_frag<XT, TY>(s.x[hh][m]);
-              const f4v sum = mfma16<TY>(x[hh][m], ones, f4v{0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-              for (int r = 0; r < 4; ++r) off[hh][m][r] = -kQ4Offset * sum[r];
-            }
+            for (int r = 0; r < 4; ++r) off[m][r] = -kQ4Offset * sum[r];
+          }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const uint32_t word = s.w[i];
@@ -295,28 +298,34 @@ __device__ void u_block(const FewArgs& a, int g, int nb, bool real, float* red) 
             const float sc = scale_at(s.s, i);
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-              const f4v p0 = mfma16<TY>(x[0][m], b, off[0][m]);
-              const f4v p1 = mfma16<TY>(x[1][m], b, off[1][m]);
+              f4v p = mfma16<TY>(x[2 * m], b, off[2 * m]);
+              if constexpr (T8 > 1) {
+                const f4v p1 = mfma16<TY>(x[2 * m + 1], b, off[2 * m + 1]);
 #pragma unroll
-              for (int r = 0; r < 4; ++r) acc[i][m][r] += sc * (h ? p1[r] : p0[r]);
+                for (int r = 0; r < 4; ++r) p[r] = first ? p[r] : p1[r];
+              }
+#pragma unroll
+              for (int r = 0; r < 4; ++r) acc[i][m][r] += sc * p[r];
             }
           }
         });
-    // the two halves of a column sit 8 lanes apart
+    // the other half's quarter sits at the other q / 2 and the other l / 8
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         f4v v;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) v[r] = acc[i][m][r] + __shfl_xor(acc[i][m][r], 8);
-        if (h == 0) *reinterpret_cast<f4v*>(red + ((wave * 4 + i) * MT + m) * 128 + (8 * q + l) * 4) = v;
+        for (int r = 0; r < 4; ++r) v[r] = acc[i][m][r] + __shfl_xor(acc[i][m][r], 40);
+        if (q < 2)
+          *reinterpret_cast<f4v*>(red + ((wave * 4 + i) * MT + m) * 128 + (16 * h + 8 * q + (l & 7)) * 4) = v;
       }
     __syncthreads();
     for (int v = tid; v < (real ? a.T * 32 : 0); v += UW * 64) {
-      const int row = v >> 5, col = v & 31, r = row & 15;
+      const int row = v >> 5, col = v & 31, r = row & 7;
       if (nb * 32 + col >= cols) continue;
-      const int at = ((col & 3) * MT + (row >> 4)) * 128 + (8 * (r >> 2) + (col >> 2)) * 4 + (r & 3);
+      const int at =
+          ((col & 3) * MT + (row >> 4)) * 128 + (2 * (row & 8) + 8 * (r >> 2) + (col >> 2)) * 4 + (r & 3);
       float s = 0.f;
 #pragma unroll
       for (int w = 0; w < UW; ++w) s += red[w * 4 * MT * 128 + at];
@@ -325,6 +334,11 @@ __device__ void u_block(const FewArgs& a, int g, int nb, bool real, float* red) 
   } else {
     constexpr int es = TY == DT_F32 ? 4 : 2;
     // fragment 4 u + q of the block, lane half h, columns 16 c + l: depth 64 u + 32 h + 8 q ..
+    constexpr int MT = (T8 + 1) / 2;  // tiles of 16 tokens
+    const XE* xp[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+      xp[m] = static_cast<const XE*>(a.X) + static_cast<long>(min(16 * m + l, a.T - 1)) * a.d + 8 * q;
     const char* wp =
         static_cast<const char*>(a.At) + (g * a.at_gs + ((static_cast<long>(nb) * (a.d / 16) + q) * 64 + l) * 8) * es;
     f4v acc[2][MT];
@@ -638,8 +652,9 @@ __host__ __device__ inline int select_chunk(int T, int NC) {
 
 // grid: the score blocks (16 columns x nsplit depth parts) first, then with
 // u_all one workgroup per two blocks of 32 factor columns of every group.
-template <int XT, int TY, int RS, int MT>
+template <int XT, int TY, int RS, int T8>
 __global__ __launch_bounds__(NT) void few_route_kernel(FewArgs a) {
+  constexpr int MT = (T8 + 1) / 2;
   extern __shared__ __attribute__((aligned(16))) float red[];  // partial tiles, then scores; last the lists' tables
   __shared__ SelectLds s;
   const int NC = a.G + (a.K > 1 ? a.G * a.K : 0);
@@ -648,7 +663,7 @@ __global__ __launch_bounds__(NT) void few_route_kernel(FewArgs a) {
     if constexpr (RS != RS_NONE) {
       const int nbu = (a.K * a.Pin * 16 + 31) / 32, half = wave_id() / UW;
       const int ub = 2 * (blockIdx.x - nsb) + half;
-      u_block<XT, TY, RS == RS_INT4, MT>(a, ub / nbu, ub % nbu, ub < a.G * nbu, red + half * UW * 2 * MT * 256);
+      u_block<XT, TY, RS == RS_INT4, T8>(a, ub / nbu, ub % nbu, ub < a.G * nbu, red + half * UW * 2 * MT * 256);
     }
     return;
   }
@@ -697,8 +712,9 @@ __global__ __launch_bounds__(NT) void few_route_kernel(FewArgs a) {
 
 // U of the chosen experts only: one workgroup per two blocks of 32 factor
 // columns, idle where none of the columns' experts is chosen.
-template <int XT, int TY, int RS, int MT>
+template <int XT, int TY, int RS, int T8>
 __global__ __launch_bounds__(NT) void few_u_kernel(FewArgs a) {
+  constexpr int MT = (T8 + 1) / 2;
   extern __shared__ __attribute__((aligned(16))) float red[];
   __shared__ int hit[2];
   const int nbu = (a.K * a.Pin * 16 + 31) / 32, half = wave_id() / UW, tid = threadIdx.x % (UW * 64);
@@ -712,7 +728,7 @@ __global__ __launch_bounds__(NT) void few_u_kernel(FewArgs a) {
   }
   __syncthreads();
   if (!hit[0] && !hit[1]) return;
-  u_block<XT, TY, RS == RS_INT4, MT>(a, g, nb, hit[half] != 0, red + half * UW * 2 * MT * 256);
+  u_block<XT, TY, RS == RS_INT4, T8>(a, g, nb, hit[half] != 0, red + half * UW * 2 * MT * 256);
 }
 
 // ------------------------------------------------------------------- up --
@@ -1477,8 +1493,9 @@ hipError_t go(K kernel, unsigned grid, unsigned threads, size_t lds, const FewAr
   return hipGetLastError();
 }
 
-template <int XT, int TY, int RS, int MT>
-hipError_t route_mt(const FewArgs& a, hipStream_t st) {
+template <int XT, int TY, int RS, int T8>
+hipError_t route_t8(const FewArgs& a, hipStream_t st) {
+  constexpr int MT = (T8 + 1) / 2;
   const int NC = a.G + (a.K > 1 ? a.G * a.K : 0);
   const unsigned nsb = (NC + 15) / 16 * a.nsplit, nub = (a.G * ((a.K * a.Pin * 16 + 31) / 32) + 1) / 2;
   const size_t tiles = static_cast<size_t>(NW) * 2 * MT * 256 * sizeof(float);  // of u_block
@@ -1489,9 +1506,9 @@ hipError_t route_mt(const FewArgs& a, hipStream_t st) {
   size_t lds = RS != RS_NONE && a.u_all ? tiles : 0;
   if (scores > lds) lds = scores;
   if (tables > lds) lds = tables;
-  hipError_t e = go(few_route_kernel<XT, TY, RS, MT>, nsb + (RS != RS_NONE && a.u_all ? nub : 0), NT, lds, a, st);
+  hipError_t e = go(few_route_kernel<XT, TY, RS, T8>, nsb + (RS != RS_NONE && a.u_all ? nub : 0), NT, lds, a, st);
   if constexpr (RS != RS_NONE)
-    if (e == hipSuccess && !a.u_all) e = go(few_u_kernel<XT, TY, RS, MT>, nub, NT, tiles, a, st);
+    if (e == hipSuccess && !a.u_all) e = go(few_u_kernel<XT, TY, RS, T8>, nub, NT, tiles, a, st);
   return e;
 }
 template <int XT, int TY, bool Q4, int RS, int MT>
@@ -1535,7 +1552,11 @@ hipError_t down_rs(const FewArgs& a, hipStream_t st) {
 
 template <int XT, int TY, bool Q4, int RS>
 hipError_t pass(const FewArgs& a, hipStream_t st) {
-  hipError_t e = a.T <= 16 ? route_mt<XT, TY, RS, 1>(a, st) : route_mt<XT, TY, RS, 2>(a, st);
+  // eights of tokens: only 4-bit input factors tell 1 from 2
+  constexpr int one = RS == RS_INT4 ? 1 : 2;
+  hipError_t e = a.T <= 8    ? route_t8<XT, TY, RS, one>(a, st)
+                 : a.T <= 16 ? route_t8<XT, TY, RS, 2>(a, st)
+                             : route_t8<XT, TY, RS, 4>(a, st);
   if (e == hipSuccess) e = a.T <= 16 ? up_mt<XT, TY, Q4, RS, 1>(a, st) : up_mt<XT, TY, Q4, RS, 2>(a, st);
   if (e == hipSuccess) e = down_rs<XT, hidden_type(TY, Q4), Q4, RS>(a, st);
   return e;
