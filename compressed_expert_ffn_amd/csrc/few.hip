@@ -762,19 +762,20 @@ __global__ __launch_bounds__(NWV * 64) void few_up_kernel(FewArgs a) {
   const int member = __builtin_amdgcn_ds_permute(4 * (grow >= 0 ? place : 63), lane);  // lane i: the i-th
   // The wavefront's jobs: a touched expert and up to 16 of its tokens, expert
   // first + wave, + NWV, ...  (beyond 16 tokens in the batch the expert's own
-  // are drawn together first, so few experts need a second job).  Their
-  // operands are few but cold, and behind a stream that fills the memory's
-  // queues a load takes microseconds: the first job's are read with the first
-  // weights, the next one's while a job runs.
+  // are drawn together first, and where the group has more than 16 the second
+  // jobs of all its experts follow the first ones).  Their operands are few but
+  // cold, and behind a stream that fills the memory's queues a load takes
+  // microseconds: the first job's are read with the first weights, the next
+  // one's while a job runs.
   struct Job {
-    int slot;
+    int e, slot;
     float wgt;
     u4v b[2][TY == DT_F32 ? 2 : 1], s[2], ad[2];  // 4-bit: words in elements 0
     u2v as;
   } job;
   int je = 0, jslot = -1;  // expert, and the slot of the lane's token
   auto job_find = [&](int j) {
-    const int i = first + j / MT;
+    const int i = first + (MT == 2 && j >= ne ? j - ne : j);
     je = a.elist[1 + i];
     if constexpr (MT == 1) {
       jslot = l < a.T ? a.eslot[i * FEW_MAX_T + l] : -1;
@@ -784,13 +785,14 @@ __global__ __launch_bounds__(NWV * 64) void few_up_kernel(FewArgs a) {
       // the p-th of the expert's tokens to lane p (lanes without one to lane 63)
       const int to = slot >= 0 ? __popc(m & ((1u << lane) - 1)) : 63;
       const int packed = __builtin_amdgcn_ds_permute(4 * to, slot);
-      const int from = 16 * (j % MT) + l;
+      const int from = (j >= ne ? 16 : 0) + l;
       const int mine = __shfl(packed, from);
       jslot = from < __popc(m) ? mine : -1;
     }
   };
   auto job_load = [&](Job& J) {
     J.slot = jslot;
+    J.e = je;
     if (MT > 1 && !__any(jslot >= 0)) return;
     J.wgt = a.w[max(jslot, 0)];
     constexpr int es = TY == DT_F32 ? 4 : 2;
@@ -815,7 +817,7 @@ __global__ __launch_bounds__(NWV * 64) void few_up_kernel(FewArgs a) {
     if constexpr (int4r)
       J.as = *reinterpret_cast<const u2v*>(a.Ad_s + (static_cast<long>(je) * (a.f / 32) + (f0 >> 5)) * RPAD + 4 * q);
   };
-  const int jobs = RS != RS_NONE ? ne * MT : 0;
+  const int jobs = RS != RS_NONE ? (MT == 2 && n > 16 ? 2 * ne : ne) : 0;
   if constexpr (RS != RS_NONE)
     if (wave < jobs) job_find(wave);
   auto between = [&]() {
@@ -979,7 +981,6 @@ __global__ __launch_bounds__(NWV * 64) void few_up_kernel(FewArgs a) {
     // row per (token, expert), to be summed per token.
     float* hw = red;  // [tokens of the group][ke][FT]
     for (int j = wave; j < jobs; j += NWV) {
-      const int e = je;
       const Job J = job;
       const bool on = J.slot >= 0;
       const int t = on ? div_small(J.slot, a.over_k) : 0, i = __popc(members & ((1u << t) - 1));
@@ -988,7 +989,7 @@ __global__ __launch_bounds__(NWV * 64) void few_up_kernel(FewArgs a) {
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const float* up =
-            a.U + (static_cast<long>(t) * a.E + e) * Pin * 16 + (Pin == 2 ? x : 0) * 16 + 8 * (q & 1);
+            a.U + (static_cast<long>(t) * a.E + J.e) * Pin * 16 + (Pin == 2 ? x : 0) * 16 + 8 * (q & 1);
         const f4v u0 = *reinterpret_cast<const f4v*>(up), u1 = *reinterpret_cast<const f4v*>(up + 4);
 #pragma unroll
         for (int r = 0; r < 8; ++r) u[x][r] = r < 4 ? u0[r] : u1[r - 4];
