@@ -160,6 +160,11 @@ def prepare(case, seed):
         from compressed_expert_ffn_amd import _lib as L
         cfg = L.make_config(T, d, f, G, K, c["kg"], c["ke"], r, c["act"], c["x"], c["base"], c["resid"])
         inputs = {k: st.pop(k) for k in ("W_grp", "W_exp", "group_bias", "expert_bias", "base", "A", "B")}
+        # codes and scales as the plain form has them: the layer rounds their values to themselves, where it may
+        # round the floats to a neighbour (a tie, or a scale's last bit)
+        for k, kind in (("base", c["base"]), ("A", c["resid"]), ("B", c["resid"])):
+            if kind == "int4_g32":
+                inputs[k] = [_values(_quantise(m)) for m in inputs[k]]
         st["layer"] = L.Layer(cfg, inputs, on_device=True)
         st["Y"] = torch.empty((T, d), dtype=DT[c["x"]], device=dev)
         k = c["kg"] * c["ke"]
