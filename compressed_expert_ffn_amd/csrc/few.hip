@@ -531,9 +531,7 @@ __device__ __forceinline__ void make_masks(const FewArgs& a, SelectLds& s) {
 }
 
 // The caller's lists, from the masks: an entry's place in its bin's list is
-// the entries of lower bins and those of lower tokens in its own.  (Counting
-// both by a loop over all entries took 7 us of a launch at T = 32, 8 experts
-// each.)
+// the entries of lower bins and those of lower tokens in its own.
 __device__ __forceinline__ void caller_lists(const FewArgs& a, SelectLds& s) {
   const int tid = threadIdx.x, wave = wave_id(), lane = tid & 63;
   __syncthreads();  // pos is free
@@ -652,6 +650,14 @@ __host__ __device__ inline int select_chunk(int T, int NC) {
 
 // grid: the score blocks (16 columns x nsplit depth parts) first, then with
 // u_all one workgroup per two blocks of 32 factor columns of every group.
+//
+// Bound by the chain of its latencies: scores (3 us at T = 1, 6 at 32, where
+// the 32 rows' loads and fp32 MFMAs count), their way through memory and the
+// ticket (1.5), reading them back (1.2 to 3.8), the selection (2 to 3), the
+// lists (0.4 at T = 1, else 1.6).  d = 4096, 16 groups of 16 experts, 4-bit
+// factors: 9.6 us at T = 1 with 19 MB read, 15.0 at T = 16, 23 at T = 32,
+// where the factors' products are the longer side (they decode 256 experts
+// for all rows: 21.8 us by themselves).
 template <int XT, int TY, int RS, int T8>
 __global__ __launch_bounds__(NT) void few_route_kernel(FewArgs a) {
   constexpr int MT = (T8 + 1) / 2;
@@ -735,6 +741,12 @@ __global__ __launch_bounds__(NT) void few_u_kernel(FewArgs a) {
 // grid: (touched group a) x (blocks of FT = 32 / Pin columns of f).  A
 // workgroup's 32 weight columns are 16 of the gate and the same 16 of the up
 // projection (SwiGLU), or 32 of the one input projection (GELU).
+//
+// Bound by the weights' bytes where they are many (d = 4096, f = 14336, bf16,
+// T = 2: 123 us a launch, about 6 TB/s), by the ramp of one round of workgroups
+// where they are few (50 MB, T = 1: 14.1 us, 3.6 TB/s; 4-bit, 14 MB: 8.4 us,
+// 1.7 TB/s), and beyond 16 tokens by the experts' jobs behind the stream
+// (fine-grained 4-bit layer, T = 32: 16.6 us, of which the stream is 11).
 template <int XT, int TY, bool Q4, int RS, int MT, int NWV>
 __global__ __launch_bounds__(NWV * 64) void few_up_kernel(FewArgs a) {
   using XE = typename Elem<XT>::T;
@@ -1069,7 +1081,8 @@ __global__ __launch_bounds__(NWV * 64) void few_up_kernel(FewArgs a) {
 
 // ---------------------------------------------------------------- v sum --
 // V = the partials of h A_down summed over the blocks of f: 64 sums per
-// workgroup, their partials dealt to 16 wavefronts.
+// workgroup, their partials dealt to 16 wavefronts.  Latency: 4.7 us for 0.8 MB
+// (T = 16, 8 experts a token, 96 blocks).
 __global__ __launch_bounds__(NT) void few_vsum_kernel(FewArgs a) {
   __shared__ float part[NW][64];
   const int nv = a.T * a.k * 16, nfb = a.f * a.Pin / 32;
@@ -1102,6 +1115,10 @@ __global__ __launch_bounds__(NT) void few_vsum_kernel(FewArgs a) {
 // where a piece ends.  Measured (us a pass, tiles of all tokens in every
 // group / pieces; d = 4096, f = 1536, 16 groups): T = 32 fp16 base 134 / 126,
 // 4-bit base 107 / 92, T = 9 fp16 70.1 / 71.2.
+//
+// Bound by the weights' bytes like the up product (d = 4096, f = 14336, bf16,
+// T = 2: 60 us a launch, about 6 TB/s; 25 MB, T = 1: 8.8 us, 2.9 TB/s), in
+// 4 bits and beyond 8 tokens by the hidden sums' loads, one line a row.
 //
 // The residual tail V B_down is more depth of the same product: two touched
 // experts' 16 rank columns are one 32-deep step, whose rows are the V of the
