@@ -312,6 +312,28 @@ def test_a_four_bit_base_runs_nowhere_else():
         lay.close()
 
 
+@pytest.mark.parametrize("case", [
+    ("swiglu", "f16", "f16", "none", 0, (250, 1), 8, 1, 32, 64, 64),
+    ("swiglu", "f16", "f16", "int4_g32", 3, (100, 10), 4, 4, 32, 64, 64),
+    ("gelu_tanh", "bf16", "bf16", "int4_g32", 16, (17, 17), 3, 5, 24, 128, 64),
+    ("swiglu", "f16", "f16", "int4_g32", 16, (1, 16), 1, 16, 32, 128, 64),
+], ids=["groups", "slots", "past16", "one_group"])
+def test_most_groups_and_slots(case):
+    """The largest tables, more candidates than a row of lanes, a group that every token chooses."""
+    import torch
+    say("[few]", case)
+    w, layer, lay, X = make(*case)
+    try:
+        rt = O.route(layer)
+        bufs = lay.route_buffers(w.T)
+        Y = lay.forward_few(X, route_bufs=bufs)
+        torch.cuda.synchronize()
+        check_routing(route_to_host(bufs), rt, w, w.T)
+        check_y(Y, O.forward(layer, routing=rt), w.x_dtype)
+    finally:
+        lay.close()
+
+
 def test_rows_behind_the_last_token_stay():
     import torch
     w, layer, lay, X = make("swiglu", "f16", "f16", "int4_g32", 16, (4, 4), 2, 2, 11, 256, 192)
