@@ -360,6 +360,20 @@ class Layer:
                                       C.c_void_p(Y.data_ptr()), rop, _stream_ptr(stream)))
         return Y
 
+    def _check_route_buffers(self, bufs, T: int):
+        import torch
+        c, i32, device = self.cfg, torch.int32, self.device
+        for name, t in bufs.items():
+            if t is None:
+                continue
+            need = (T * self.k if name in ("idx", "w", "perm") else T * c.top_groups if name in ("gidx", "gperm") else
+                    self.E + (name == "offsets") if name in ("counts", "offsets") else
+                    c.G + (name == "goffsets") if name in ("gcounts", "goffsets") else -1)
+            if (need < 0 or t.numel() < need or t.dtype is not (torch.float32 if name == "w" else i32) or
+                    t.get_device() != device or not t.is_contiguous()):
+                raise ValueError(f"route_bufs[{name!r}]: expected the buffers of route_buffers({T}) on device {device}, "
+                                 f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+
     def forward_few(self, X, Y=None, route_bufs=None, stream=None):
         """moe_forward_few: the layer for up to 32 tokens."""
         T, d = X.shape if X.dim() == 2 else (0, -1)
@@ -371,7 +385,10 @@ class Layer:
         elif Y.shape != X.shape or Y.dtype is not X.dtype or not Y.is_contiguous() or Y.get_device() != self.device:
             raise ValueError(f"Y: expected contiguous {X.dtype} {tuple(X.shape)} on {X.device}, got {Y.dtype} "
                              f"{tuple(Y.shape)} on {Y.device}")
-        rop = None if route_bufs is None else C.byref(self._route_struct(route_bufs))
+        rop = None
+        if route_bufs:
+            self._check_route_buffers(route_bufs, T)
+            rop = C.byref(self._route_struct(route_bufs))
         rc = lib.moe_forward_few(self.h, X.data_ptr(), T, Y.data_ptr(), rop, _raw_stream(stream, self.device))
         if rc:
             check(rc)

@@ -281,6 +281,13 @@ def test_no_tokens_and_refusals():
         for args in ((X.data_ptr() + 2, 1, X.data_ptr() + 512), (X.data_ptr(), 1, X.data_ptr()), (None, 1, X.data_ptr()),
                      (X.data_ptr(), 1, None), (X.data_ptr(), -1, X.data_ptr() + 512), (X.data_ptr(), 1, X.data_ptr() + 513)):
             assert L.lib.moe_forward_few(lay.h, args[0], args[1], args[2], None, None) == L.MOE_ERR_INVALID_ARG, args
+        bad = lay.route_buffers(8)
+        with pytest.raises(ValueError, match="idx"):
+            lay.forward_few(X, route_bufs=lay.route_buffers(X.shape[0] - 1))
+        for name, t in (("w", bad["w"].int()), ("counts", bad["counts"].cpu()), ("gperm", bad["gperm"][::2]),
+                        ("other", bad["idx"])):
+            with pytest.raises(ValueError, match=name):
+                lay.forward_few(X[:8].contiguous(), route_bufs={name: t})
         lay.offload_enable(2)
         with pytest.raises(L.MoEError, match="offloaded"):
             lay.forward_few(X)
