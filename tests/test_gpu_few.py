@@ -423,3 +423,66 @@ def test_two_handles_on_two_streams():
     finally:
         for _, _, lay, _ in made:
             lay.close()
+
+
+@pytest.mark.parametrize("xd", ["f16", "bf16"])
+def test_a_decode_block_of_both_operators(xd):
+    """Steps of a decode loop: a 4-bit projection, the layer with a 4-bit base
+    and its sum with the projection, a 4-bit output head whose best column is
+    the next token.  Eager and as a captured graph; every operator against 64
+    bits on the input it was given."""
+    import torch
+    L = _lib()
+    T, d, vocab = 3, 256, 67
+    w, layer, lay, X0 = make("swiglu", xd, "int4_g32", "int4_g32", 16, (4, 4), 2, 2, T, d, 192)
+    rng = np.random.default_rng(7)
+
+    def linear(n_out):
+        q = rng.integers(-8, 8, (d, n_out)).astype(np.int8)
+        scale = np.full((d // 64, n_out), 1 / (4.6 * np.sqrt(d)), np.float16)
+        ref = q * np.repeat(scale.astype(np.float64), 64, axis=0)
+        return L.QuantLinear(d, n_out, 64, xd, q=q, scale=scale), ref
+
+    (proj, Wp), (head, Wh) = linear(d), linear(vocab)
+    try:
+        emb = torch.from_numpy(rng.standard_normal((vocab, d)).astype(np.float32)).cuda().to(X0.dtype)
+        X = torch.empty_like(X0)
+        H, M, Z = torch.empty_like(X0), torch.empty_like(X0), torch.empty((T, vocab), dtype=X0.dtype, device="cuda")
+
+        def step():
+            proj.matvec(X, H)
+            lay.forward_few(H, M)
+            M.add_(H)
+            head.matvec(M, Z)
+
+        def run(call):
+            tok, seen = torch.tensor([5, 40, 66], device="cuda"), []
+            for _ in range(4):
+                X.copy_(emb[tok])
+                call()
+                tok = Z.argmax(1)
+                seen.append([t.clone() for t in (X, H, M, Z, tok)])
+            torch.cuda.synchronize()
+            return seen
+
+        eager = run(step)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step()
+        for a, b in zip(eager, run(g.replay)):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+        for x, h, m, z, _ in eager:
+            x, m = y_to_host(x), y_to_host(m)
+            hd = y_to_host(h)
+            check_y(h, x @ Wp, xd)
+            host = h.cpu().view(torch.int16).numpy()
+            moe = O.forward(dict(layer, X=host.view(np.float16) if xd == "f16" else host.view(np.uint16)))
+            # the layer's result and the sum are each rounded once
+            ref = moe + hd
+            assert (np.abs(m - ref) <= STEP[xd] * (np.abs(moe) * 1.05 + np.abs(ref) * 1.05 + 0.05 *
+                                                   np.abs(moe).max())).all()
+            check_y(z, m @ Wh, xd)
+    finally:
+        proj.close()
+        head.close()
+        lay.close()
